@@ -19,9 +19,16 @@
  *        or
  *        vdit_attn_divided_time  attention over the T tokens at each spatial site
  *        vdit_attn_divided_space attention over the H'*W' tokens of each frame
+ *        or
+ *        vdit_attn_select_blocks a cheap score picks the key blocks of each block
+ *        vdit_attn_block_sparse  of queries, which then attends to those alone
  *     -> vdit_attn_cross         the video tokens attend to the text tokens' keys
  *                                and values (the block's second attention)
  *   and at the end: vdit_unpatchify_3d, tokens back to the latent clip
+ *
+ * and, for training the attention sub-layer, the gradients of its steps:
+ *   vdit_attn_block_sparse_bwd, then vdit_qk_norm_rope_3d_bwd or
+ *   vdit_rope_3d_bwd
  *
  * Sources (page title, section):
  *   [towardsai]  "How AI Generates Video: Inside Sora and Wan2.1 on a Real GPU",
@@ -334,6 +341,130 @@ int vdit_attn_divided_space(const void* q, const void* k, const void* v, void* o
 int vdit_attn_cross(const void* q, const void* k, const void* v, void* o, float* lse,
                     int B, int Lq, int Lk, int heads, int head_dim, float scale,
                     vdit_stream_t stream);
+
+/*
+ * vdit_attn_select_blocks - a cheap score picks the key blocks that each block
+ * of queries attends to (the input of vdit_attn_block_sparse).
+ *
+ * Blocks are 128 consecutive tokens; the last block of a sequence may be
+ * shorter.  For each batch, head, query block i and key block j
+ *   score[i, j] = (mean of Q over block i) . (mean of K over block j)
+ * and blocks[b, h, i, j] = 1 for the top_k key blocks of highest score in row
+ * i, else 0; of equal scores the lower j goes first, and a NaN score goes behind
+ * every number.  A positive scale of the scores would not change the choice, so
+ * there is none.  Means and scores are float64.
+ * q: [B, Lq, heads, head_dim], k: [B, Lk, heads, head_dim], bfloat16, 16-byte
+ * aligned; blocks: bytes [B, heads, ceil(Lq/128), ceil(Lk/128)], every one
+ * written; workspace: vdit_attn_select_blocks_workspace bytes, 16-byte aligned,
+ * used by this call alone until the stream has run it.
+ * Errors: VDIT_ERR_NULL, VDIT_ERR_SHAPE (also: top_k below 1 or above
+ * ceil(Lk/128)), VDIT_ERR_ALIGN, VDIT_ERR_UNSUPPORTED (head_dim; more than
+ * 6,144 key blocks), VDIT_ERR_CUDA.
+ * Watchdog: device-wide (see the conventions above).
+ */
+int vdit_attn_select_blocks(const void* q, const void* k, void* blocks, void* workspace,
+                            int B, int Lq, int Lk, int heads, int head_dim, int top_k,
+                            vdit_stream_t stream);
+
+/* Workspace bytes of vdit_attn_select_blocks, or -1 for a bad size.  Host only. */
+long long vdit_attn_select_blocks_workspace(int B, int Lq, int Lk, int heads, int head_dim);
+
+/*
+ * vdit_attn_block_sparse - attention of each block of 128 queries over the
+ * blocks of 128 keys that a mask marks for it.
+ *
+ *   O[b, i, h, :] = sum_j softmax_j(scale * Q[b,i,h,:] . K[b,j,h,:]) V[b, j, h, :]
+ *
+ * with j over the keys of the blocks that have
+ * blocks[b, h, i / 128, j / 128] != 0 (bytes [B, heads, ceil(Lq/128),
+ * ceil(Lk/128)]; vdit_attn_select_blocks writes such a mask, and masks may be
+ * combined byte by byte).  A query whose row of the mask is empty gets O = 0 and
+ * a log-sum-exp of -inf.  Keys of unmarked blocks are never read, whatever they
+ * hold.  q, o: [B, Lq, heads, head_dim]; k, v: [B, Lk, heads, head_dim] (Lq and
+ * Lk need not agree: one query token over a long sequence of keys is shared by
+ * several CTAs); lse: NULL or [B, heads, Lq].  o must not overlap q, k or v.
+ * With every block marked this is vdit_attn_cross; numerics and alignment are
+ * those of vdit_attn_full.  The result does not change from run to run.
+ * Errors: VDIT_ERR_NULL, VDIT_ERR_SHAPE, VDIT_ERR_ALIGN, VDIT_ERR_UNSUPPORTED
+ * (head_dim; more than 6,144 key blocks), VDIT_ERR_CUDA.
+ * Watchdog: device-wide (see the conventions above).
+ */
+int vdit_attn_block_sparse(const void* q, const void* k, const void* v, const void* blocks,
+                           void* o, float* lse,
+                           int B, int Lq, int Lk, int heads, int head_dim, float scale,
+                           vdit_stream_t stream);
+
+/*
+ * vdit_attn_block_sparse_bwd - the gradients of vdit_attn_block_sparse.
+ *
+ * With P = exp(scale * Q K^T - lse) over the marked blocks and d_o the gradient
+ * of O:
+ *   delta = rowsum(d_o o O)     dS = P o (d_o V^T - delta)
+ *   dQ = scale * dS K           dK = scale * dS^T Q           dV = P^T d_o
+ * o and lse are what the forward call wrote for the same q, k, v, blocks and
+ * scale (lse is required).  Every element of dq, dk and dv is written: rows
+ * that take part in nothing get zeros.  Sums are float32; P and dS are rounded
+ * to bfloat16 as operands of the products, the gradients once at the end.  No
+ * atomics: the result does not change from run to run.  With every block marked
+ * these are the gradients of vdit_attn_full and vdit_attn_cross.
+ * q, o, d_o, dq: [B, Lq, heads, head_dim]; k, v, dk, dv: [B, Lk, heads,
+ * head_dim]; lse: [B, heads, Lq]; workspace:
+ * vdit_attn_block_sparse_bwd_workspace bytes, used by this call alone until
+ * the stream has run it; all 16-byte aligned (lse 4-byte).  dq, dk and dv must
+ * not overlap each other or any input.
+ * Errors: VDIT_ERR_NULL, VDIT_ERR_SHAPE, VDIT_ERR_ALIGN, VDIT_ERR_UNSUPPORTED
+ * (head_dim; more than 6,144 query or key blocks), VDIT_ERR_CUDA.
+ * Watchdog: device-wide (see the conventions above).
+ */
+int vdit_attn_block_sparse_bwd(const void* q, const void* k, const void* v, const void* blocks,
+                               const void* o, const float* lse, const void* d_o,
+                               void* dq, void* dk, void* dv, void* workspace,
+                               int B, int Lq, int Lk, int heads, int head_dim, float scale,
+                               vdit_stream_t stream);
+
+/* Workspace bytes of vdit_attn_block_sparse_bwd, or -1 for a bad size.  Host only. */
+long long vdit_attn_block_sparse_bwd_workspace(int B, int Lq, int heads);
+
+/*
+ * vdit_rope_3d_bwd - the gradients of vdit_rope_3d: each pair of gq and gk is
+ * turned back by its token's angle,
+ *     dx[2i]   = g[2i]*cos(a) + g[2i+1]*sin(a)
+ *     dx[2i+1] = g[2i+1]*cos(a) - g[2i]*sin(a)
+ * with the angles, the rounding and everything else of vdit_rope_3d (in place
+ * allowed; gq and dq both NULL: K alone).
+ * Watchdog: device-wide (see the conventions above).
+ */
+int vdit_rope_3d_bwd(const void* gq, const void* gk, void* dq, void* dk,
+                     int B, int Tg, int Hg, int Wg, int heads, int head_dim,
+                     int d_t, int d_h, int d_w, float theta, vdit_stream_t stream);
+
+/*
+ * vdit_qk_norm_rope_3d_bwd - the gradients of vdit_qk_norm_rope_3d.
+ *
+ * For one group of N = norm_group channels x with weight w, r = 1 / sqrt(mean(x^2)
+ * + eps), and g the gradient of the rotated result, turned back as by
+ * vdit_rope_3d_bwd to u:
+ *   dx = r * (u w) - x * r^3 * mean(x u w)        dw = sum of u x r
+ * (dw over all tokens and, with a per-head group, over the heads).
+ * q, k: the forward call's inputs; gq, gk: the gradients of its outputs; wq, wk
+ * as there (NULL: weight 1).  dwq, dwk: float32 [norm_group] or NULL (not
+ * wanted); with both NULL workspace may be NULL, else it has
+ * vdit_qk_norm_rope_3d_bwd_workspace bytes, 16-byte aligned, used by this call
+ * alone until the stream has run it.  q, gq and dq all NULL: K alone (dwq is then
+ * not written).  dq and dk must not overlap any input.  float32 throughout, dq
+ * and dk rounded once to bfloat16; the sums of dwq and dwk are taken in a fixed
+ * order, so they do not change from run to run.
+ * Errors as for vdit_qk_norm_rope_3d.
+ * Watchdog: device-wide (see the conventions above).
+ */
+int vdit_qk_norm_rope_3d_bwd(const void* q, const void* k, const void* gq, const void* gk,
+                             void* dq, void* dk, const float* wq, const float* wk,
+                             float* dwq, float* dwk, void* workspace, int norm_group, float eps,
+                             int B, int Tg, int Hg, int Wg, int heads, int head_dim,
+                             int d_t, int d_h, int d_w, float theta, vdit_stream_t stream);
+
+/* Workspace bytes of vdit_qk_norm_rope_3d_bwd, or -1 for a bad group.  Host only. */
+long long vdit_qk_norm_rope_3d_bwd_workspace(int norm_group);
 
 /* Text for a status code (static storage; never NULL). */
 const char* vdit_status_string(int status);

@@ -21,9 +21,16 @@ Calls (see ``include/vdit.h`` for the exact definitions and sources):
 * :func:`attn_divided_time`   attention over the T tokens of each spatial site
 * :func:`attn_divided_space`  attention over the HW tokens of each frame
 * :func:`attn_cross`          video tokens attending to a separate key/value sequence
+* :func:`attn_select_blocks`  a cheap score picks each query block's key blocks
+* :func:`attn_block_sparse`   attention over the key blocks picked for each query block
+
+and the gradients of the attention sub-layer's steps:
+
+* :func:`attn_block_sparse_bwd`, :func:`rope_3d_bwd`, :func:`qk_norm_rope_3d_bwd`
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -31,11 +38,13 @@ import torch
 
 __all__ = ["VditError", "lib", "patchify_3d", "patch_embed_3d", "unpatchify_3d", "rope_3d",
            "qk_norm_rope_3d", "rope_3d_table", "attn_full", "attn_full_rope_q", "attn_divided_time", "attn_divided_space", "attn_cross",
-           "device_status", "watchdog_selftest", "status_string", "default_split", "LIB_PATH"]
+           "attn_select_blocks", "attn_block_sparse", "attn_block_sparse_bwd", "rope_3d_bwd", "qk_norm_rope_3d_bwd",
+           "SPARSE_BLOCK", "device_status", "watchdog_selftest", "status_string", "default_split", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvdit.so")
 
 F32, BF16 = 0, 1
+SPARSE_BLOCK = 128        # tokens of a query block and of a key block of the sparse calls
 _STATUS = {0: "VDIT_OK", 1: "VDIT_ERR_NULL", 2: "VDIT_ERR_SHAPE", 3: "VDIT_ERR_ALIGN",
            4: "VDIT_ERR_UNSUPPORTED", 5: "VDIT_ERR_CUDA", 6: "VDIT_ERR_TIMEOUT"}
 
@@ -63,6 +72,11 @@ _SIGNATURES = {
     "vdit_attn_divided_time": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P],
     "vdit_attn_divided_space": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P],
     "vdit_attn_cross": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P],
+    "vdit_attn_select_blocks": [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P],
+    "vdit_attn_block_sparse": [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P],
+    "vdit_attn_block_sparse_bwd": [_P] * 11 + [_I, _I, _I, _I, _I, _F, _P],
+    "vdit_rope_3d_bwd": [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P],
+    "vdit_qk_norm_rope_3d_bwd": [_P] * 11 + [_I, _F, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P],
     "vdit_device_status": [ctypes.POINTER(ctypes.c_uint)],
     "vdit_watchdog_selftest": [_I, _P],
     "vdit_version": [],
@@ -81,8 +95,11 @@ def lib() -> ctypes.CDLL:
             fn = getattr(L, name)
             fn.argtypes = args
             fn.restype = ctypes.c_int
-        L.vdit_rope_3d_table_entries.argtypes = [_I] * 7
-        L.vdit_rope_3d_table_entries.restype = ctypes.c_longlong
+        for name, n_args in (("vdit_rope_3d_table_entries", 7), ("vdit_attn_select_blocks_workspace", 5),
+                             ("vdit_attn_block_sparse_bwd_workspace", 3), ("vdit_qk_norm_rope_3d_bwd_workspace", 1)):
+            fn = getattr(L, name)
+            fn.argtypes = [_I] * n_args
+            fn.restype = ctypes.c_longlong
         L.vdit_status_string.argtypes = [ctypes.c_int]
         L.vdit_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -354,6 +371,210 @@ def attn_cross(q, k, v, out=None, lse=None, scale: float = 0.0, stream=None):
         q.data_ptr(), k.data_ptr(), v.data_ptr(), _dev(out, "out", torch.bfloat16), lse_p, B, Lq, Lk, Hh, D,
         float(scale), _stream(stream)))
     return out if lse_t is None else (out, lse_t)
+
+
+# --------------------------------------------------------------------------
+# Attention over selected blocks, and the gradients
+# --------------------------------------------------------------------------
+
+def _launch_stream(t: torch.Tensor, name: str, stream):
+    """(context, stream handle) for a call on ``t``'s data.  Memory that the call
+    allocates (outputs, workspace) is allocated inside the context, so that it
+    belongs to the stream the kernels run on: a workspace is dropped when the
+    call returns, and only work queued on that stream after the kernels may get
+    its memory."""
+    _dev(t, name)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return contextlib.nullcontext(), torch.cuda.current_stream().cuda_stream
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if isinstance(t, torch.Tensor) and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _like(t, given, name: str):
+    """``given``, or a new tensor, of ``t``'s shape: a bfloat16 output."""
+    if given is None:
+        return torch.empty_like(t)
+    if given.shape != t.shape:
+        raise ValueError(f"{name} must be {tuple(t.shape)}")
+    _dev(given, name, torch.bfloat16)
+    return given
+
+
+def _block_counts(q, k):
+    return tuple((t.shape[1] + SPARSE_BLOCK - 1) // SPARSE_BLOCK for t in (q, k))
+
+
+def _check_blocks(q, k, blocks, name="blocks"):
+    want = (q.shape[0], q.shape[2], *_block_counts(q, k))
+    if tuple(blocks.shape) != want:
+        raise ValueError(f"{name} must be [B, heads, ceil(Lq/128), ceil(Lk/128)] = {want}, got {tuple(blocks.shape)}")
+    if blocks.dtype not in (torch.bool, torch.uint8):
+        raise ValueError(f"{name} must be bool or uint8, got {blocks.dtype}")
+    return _dev(blocks, name)
+
+
+def _check_qk(q, k):
+    if q.dim() != 4 or k.dim() != 4 or q.shape[0] != k.shape[0] or q.shape[2:] != k.shape[2:]:
+        raise ValueError("q must be [B, Lq, heads, head_dim] and k [B, Lk, heads, head_dim]")
+    _dev(q, "q", torch.bfloat16)
+    _dev(k, "k", torch.bfloat16)
+
+
+def _workspace(n_bytes: int, device):
+    if n_bytes < 0:
+        raise ValueError("bad sizes")
+    return torch.empty(max(n_bytes, 16), dtype=torch.uint8, device=device)
+
+
+def attn_select_blocks(q, k, top_k: int, out=None, stream=None):
+    """For each block of 128 queries, the ``top_k`` blocks of 128 keys with the
+    highest product of their mean key with its mean query (ties: the lower
+    block).  q [B, Lq, heads, D], k [B, Lk, heads, D] bfloat16 -> truth values
+    [B, heads, ceil(Lq/128), ceil(Lk/128)], the ``blocks`` of
+    :func:`attn_block_sparse`; masks may be combined with ``|`` and ``&``."""
+    _check_qk(q, k)
+    _same_device(q.device, k=k, out=out)
+    ctx, st = _launch_stream(q, "q", stream)
+    B, Lq, Hh, D = q.shape
+    Lk = k.shape[1]
+    with ctx:
+        if out is None:
+            out = torch.empty((B, Hh, *_block_counts(q, k)), dtype=torch.bool, device=q.device)
+        else:
+            _check_blocks(q, k, out, "out")
+        ws = _workspace(lib().vdit_attn_select_blocks_workspace(B, Lq, Lk, Hh, D), q.device)
+        _check("vdit_attn_select_blocks", lib().vdit_attn_select_blocks(
+            q.data_ptr(), k.data_ptr(), out.data_ptr(), ws.data_ptr(), B, Lq, Lk, Hh, D, int(top_k), st))
+    return out
+
+
+def attn_block_sparse(q, k, v, blocks, out=None, lse=None, scale: float = 0.0, stream=None):
+    """Attention of each block of 128 queries over the blocks of 128 keys that
+    ``blocks`` (bool or uint8 [B, heads, ceil(Lq/128), ceil(Lk/128)]) marks for
+    it.  q [B, Lq, heads, D]; k, v [B, Lk, heads, D].  Queries with no marked
+    block get zeros (log-sum-exp -inf).  ``lse=True`` also returns [B, heads, Lq]."""
+    _check_qk(q, k)
+    bp = _check_blocks(q, k, blocks)
+    _same_device(q.device, k=k, v=v, blocks=blocks, out=out, lse=lse)
+    ctx, st = _launch_stream(q, "q", stream)
+    with ctx:
+        out, lse_t, lse_p = _attn_io(q, k, v, out, lse, cross=True)
+        B, Lq, Hh, D = q.shape
+        _check("vdit_attn_block_sparse", lib().vdit_attn_block_sparse(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), bp, _dev(out, "out", torch.bfloat16), lse_p, B, Lq, k.shape[1],
+            Hh, D, float(scale), st))
+    return out if lse_t is None else (out, lse_t)
+
+
+def attn_block_sparse_bwd(q, k, v, blocks, out, lse, d_out, scale: float = 0.0, dq=None, dk=None, dv=None,
+                          stream=None):
+    """Gradients (dq, dk, dv) of :func:`attn_block_sparse` for the gradient
+    ``d_out`` of its result, from its inputs and the ``out`` and ``lse`` it
+    returned.  With every block marked: those of full or cross-attention."""
+    _check_qk(q, k)
+    bp = _check_blocks(q, k, blocks)
+    B, Lq, Hh, D = q.shape
+    if v.shape != k.shape:
+        raise ValueError("k and v must have one shape")
+    if out.shape != q.shape or d_out.shape != q.shape:
+        raise ValueError("out and d_out must have q's shape")
+    if tuple(lse.shape) != (B, Hh, Lq):
+        raise ValueError(f"lse must be {(B, Hh, Lq)}")
+    for t, n in ((v, "v"), (out, "out"), (d_out, "d_out")):
+        _dev(t, n, torch.bfloat16)
+    _dev(lse, "lse", torch.float32)
+    _same_device(q.device, k=k, v=v, blocks=blocks, out=out, lse=lse, d_out=d_out, dq=dq, dk=dk, dv=dv)
+    ctx, st = _launch_stream(q, "q", stream)
+    with ctx:
+        dq, dk, dv = _like(q, dq, "dq"), _like(k, dk, "dk"), _like(v, dv, "dv")
+        ws = _workspace(lib().vdit_attn_block_sparse_bwd_workspace(B, Lq, Hh), q.device)
+        _check("vdit_attn_block_sparse_bwd", lib().vdit_attn_block_sparse_bwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), bp, out.data_ptr(), lse.data_ptr(), d_out.data_ptr(),
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), B, Lq, k.shape[1], Hh, D, float(scale), st))
+    return dq, dk, dv
+
+
+def _grid_and_split(k, grid, split):
+    if k.dim() != 4:
+        raise ValueError("k and gk must be [B, L, heads, head_dim]")
+    Tg, Hg, Wg = grid
+    if Tg * Hg * Wg != k.shape[1]:
+        raise ValueError("grid does not match the sequence length")
+    return (Tg, Hg, Wg), default_split(k.shape[3]) if split is None else split
+
+
+def rope_3d_bwd(gq, gk, grid, split=None, theta: float = 10000.0, dq=None, dk=None, stream=None):
+    """Gradients (dq, dk) of :func:`rope_3d` for the gradients ``gq`` and ``gk``
+    ([B, L, heads, D] bfloat16) of its results: every pair turned back.  dq may be
+    gq, and dk gk (in place); ``gq=None``: K only."""
+    grid, split = _grid_and_split(gk, grid, split)
+    if gq is not None and gq.shape != gk.shape:
+        raise ValueError("gq and gk must both be [B, L, heads, head_dim]")
+    if gq is None and dq is not None:
+        raise ValueError("dq without gq")
+    _dev(gk, "gk", torch.bfloat16)
+    _same_device(gk.device, gq=gq, dq=dq, dk=dk)
+    ctx, st = _launch_stream(gk, "gk", stream)
+    B, _, Hh, D = gk.shape
+    with ctx:
+        dk = _like(gk, dk, "dk")
+        if gq is not None:
+            _dev(gq, "gq", torch.bfloat16)
+            dq = _like(gq, dq, "dq")
+        _check("vdit_rope_3d_bwd", lib().vdit_rope_3d_bwd(
+            None if gq is None else gq.data_ptr(), gk.data_ptr(), None if gq is None else dq.data_ptr(),
+            dk.data_ptr(), B, *grid, Hh, D, *split, float(theta), st))
+    return dq, dk
+
+
+def qk_norm_rope_3d_bwd(q, k, gq, gk, grid, norm_group: int, wq=None, wk=None, eps: float = 1e-6, split=None,
+                        theta: float = 10000.0, dq=None, dk=None, stream=None):
+    """Gradients (dq, dk, dwq, dwk) of :func:`qk_norm_rope_3d`, from its inputs
+    and the gradients ``gq`` and ``gk`` of its results.  dwq and dwk are float32
+    [norm_group], None where the weight was.  ``q=None`` (and ``gq=None``): K only."""
+    grid, split = _grid_and_split(k, grid, split)
+    if (q is None) != (gq is None):
+        raise ValueError("q and gq go together")
+    if gk.shape != k.shape or (q is not None and (q.shape != k.shape or gq.shape != k.shape)):
+        raise ValueError("q, k, gq and gk must all be [B, L, heads, head_dim]")
+    if q is None and (dq is not None or wq is not None):
+        raise ValueError("dq or wq without q")
+    for t, n in ((q, "q"), (k, "k"), (gq, "gq"), (gk, "gk")):
+        if t is not None:
+            _dev(t, n, torch.bfloat16)
+    for w, n in ((wq, "wq"), (wk, "wk")):
+        if w is not None:
+            if tuple(w.shape) != (norm_group,):
+                raise ValueError(f"{n} must have norm_group entries")
+            _dev(w, n, torch.float32)
+    _same_device(k.device, q=q, gq=gq, gk=gk, wq=wq, wk=wk, dq=dq, dk=dk)
+    ctx, st = _launch_stream(k, "k", stream)
+    B, _, Hh, D = k.shape
+
+    def ptr(t):
+        return None if t is None else t.data_ptr()
+
+    with ctx:
+        dk = _like(k, dk, "dk")
+        if q is not None:
+            dq = _like(q, dq, "dq")
+        dwq, dwk = (None if w is None else torch.empty_like(w) for w in (wq, wk))
+        ws = None
+        if dwq is not None or dwk is not None:
+            ws = _workspace(lib().vdit_qk_norm_rope_3d_bwd_workspace(int(norm_group)), k.device)
+        _check("vdit_qk_norm_rope_3d_bwd", lib().vdit_qk_norm_rope_3d_bwd(
+            ptr(q), k.data_ptr(), ptr(gq), gk.data_ptr(), ptr(dq), dk.data_ptr(), ptr(wq), ptr(wk), ptr(dwq),
+            ptr(dwk), ptr(ws), int(norm_group), float(eps), B, *grid, Hh, D, *split, float(theta), st))
+    return dq, dk, dwq, dwk
 
 
 def _divided(name, q, k, v, T, HW, out, lse, scale, stream):

@@ -2,9 +2,11 @@
 
     python -m spacetime_attention_vdit_b200.build [--verbose-ptxas]
 
-The library is one translation unit (csrc/vdit_api.cu includes every kernel);
-the CUDA runtime is linked statically and the driver's tensor-map encoder is
-looked up at run time, so the .so needs no CUDA libraries on its link line.
+csrc/vdit_api.cu includes every kernel that waits (the watchdog's flag is one
+symbol of that translation unit); the block selection, whose kernels have no
+waits, is compiled on its own and linked in as an object.  The CUDA runtime is
+linked statically and the driver's tensor-map encoder is looked up at run time,
+so the .so needs no CUDA libraries on its link line.
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,7 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libvdit.so")
 SOURCES = [os.path.join(CSRC, "vdit_api.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
+OBJECT_SOURCES = [os.path.join(CSRC, "block_select.cu")]
+DEPS = SOURCES + OBJECT_SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
     os.path.join(INCLUDE, "vdit.h")]
 
 
@@ -30,13 +34,20 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libvdit.so")
 
 
-def command(ptxas_verbose: bool = False, out: str = LIB):
-    cmd = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-           "-Xcompiler", "-fPIC,-O2", "-shared", "-cudart", "static", "-I", INCLUDE, "-I", CSRC,
-           "-o", out] + SOURCES
-    if ptxas_verbose:
-        cmd[1:1] = ["-Xptxas", "-v"]
-    return cmd
+FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
+         "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC]
+
+
+def command(ptxas_verbose: bool = False, out: str = LIB, objects=()):
+    """Compile vdit_api.cu and link it with ``objects`` into the shared library."""
+    verbose = ["-Xptxas", "-v"] if ptxas_verbose else []
+    return [nvcc()] + verbose + FLAGS + ["-shared", "-cudart", "static", "-o", out] + SOURCES + list(objects)
+
+
+def object_command(source: str, out: str, ptxas_verbose: bool = False):
+    """Compile one of OBJECT_SOURCES on its own."""
+    verbose = ["-Xptxas", "-v"] if ptxas_verbose else []
+    return [nvcc()] + verbose + FLAGS + ["-c", "-o", out, source]
 
 
 def up_to_date() -> bool:
@@ -51,12 +62,16 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     if not force and not ptxas_verbose and up_to_date():
         return LIB
     tmp = LIB + ".tmp"
-    res = subprocess.run(command(ptxas_verbose, tmp), capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + res.stdout + res.stderr)
+    with tempfile.TemporaryDirectory() as folder:
+        objects = [os.path.join(folder, os.path.basename(src) + ".o") for src in OBJECT_SOURCES]
+        steps = [object_command(src, obj, ptxas_verbose) for src, obj in zip(OBJECT_SOURCES, objects)]
+        for cmd in steps + [command(ptxas_verbose, tmp, objects)]:
+            res = subprocess.run(cmd, capture_output=True, text=True)
+            if res.returncode != 0:
+                raise RuntimeError("nvcc failed:\n" + res.stdout + res.stderr)
+            if ptxas_verbose:
+                sys.stderr.write(res.stderr)
     os.replace(tmp, LIB)
-    if ptxas_verbose:
-        sys.stderr.write(res.stderr)
     return LIB
 
 

@@ -215,6 +215,7 @@ struct RopeShape {
   int pt_end, ph_end; // pair index where the h segment starts, and the w segment
   int d_t, d_h, d_w;
   int ntens;          // 2: Q and K; 1: one tensor (K), passed in the Q slots
+  float turn = 1.f;   // rope3d_kernel: 1 rotates, -1 rotates back (the gradient)
 };
 
 // (cos, sin) of pos * theta^(-2i/d) for pair i of a segment of width d: the
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope3d_kernel(const __nv_bfloat1
       else pos = l % s.Wg;
       double sn, cn;
       sincos((double)pos * inv_freq[p], &sn, &cn);
-      cs[j][p] = make_float2((float)cn, (float)sn);
+      cs[j][p] = make_float2((float)cn, s.turn * (float)sn);
     }
     __syncthreads();
 

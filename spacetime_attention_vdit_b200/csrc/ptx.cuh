@@ -38,8 +38,8 @@ __device__ __forceinline__ void watchdog_trip(int site) {
 }
 
 // Dynamic shared memory of every kernel in the library (one declaration, so that
-// all kernels agree on its alignment; kernels that need more align it themselves).
-extern __shared__ __align__(128) unsigned char dyn_smem[];
+// all kernels agree on its alignment: that of the 128-byte swizzle's pattern).
+extern __shared__ __align__(1024) unsigned char dyn_smem[];
 
 // ---------------------------------------------------------------------------
 // Shared-memory addresses and mbarriers
@@ -420,6 +420,14 @@ __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
 __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
       : "=l"(d)
       : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
   return *reinterpret_cast<float2*>(&d);

@@ -12,8 +12,12 @@
 #include <mutex>
 
 #include "vdit.h"
+#include "vdit_internal.h"
 #include "attn_tcgen05.cuh"
+#include "attn_block_sparse.cuh"
+#include "attn_block_sparse_bwd.cuh"
 #include "attn_time_short.cuh"
+#include "norm_rope_bwd.cuh"
 #include "patchify_rope.cuh"
 #include "patch_embed.cuh"
 
@@ -278,7 +282,157 @@ int check_attn_args(const void* q, const void* k, const void* v, const void* o, 
   return VDIT_OK;
 }
 
+// Q and K (or K alone) through rope3d_kernel, turned forward (turn 1) or back (-1).
+int rope_pass(const void* q_in, const void* k_in, void* q_out, void* k_out, int B, int Tg, int Hg, int Wg, int heads,
+              int head_dim, int d_t, int d_h, int d_w, float theta, float turn, vdit_stream_t stream) {
+  const bool k_only = q_in == nullptr && q_out == nullptr;
+  if (k_only) { q_in = k_in; q_out = k_out; }
+  if (!q_in || !k_in || !q_out || !k_out) return VDIT_ERR_NULL;
+  if (B <= 0 || Tg <= 0 || Hg <= 0 || Wg <= 0 || heads <= 0 || head_dim <= 0) return VDIT_ERR_SHAPE;
+  if (d_t < 0 || d_h < 0 || d_w < 0 || (d_t | d_h | d_w) & 1 || d_t + d_h + d_w != head_dim) return VDIT_ERR_SHAPE;
+  if (!(theta > 0.f) || !std::isfinite(theta)) return VDIT_ERR_SHAPE;
+  if (head_dim % 8 != 0 || head_dim / 2 > kRopeMaxPairs) return VDIT_ERR_UNSUPPORTED;
+  if (!aligned16(q_in) || !aligned16(k_in) || !aligned16(q_out) || !aligned16(k_out)) return VDIT_ERR_ALIGN;
+  const long long L = (long long)Tg * Hg * Wg;
+  if (L > 0x7fffffffLL || (double)B * (double)L * heads * head_dim > 4.0e18) return VDIT_ERR_SHAPE;
+  RopeShape s;
+  s.ntok = (long long)B * L;
+  s.L = (int)L; s.Hg = Hg; s.Wg = Wg;
+  s.heads = heads; s.D = head_dim;
+  s.pt_end = d_t / 2; s.ph_end = (d_t + d_h) / 2;
+  s.d_t = d_t; s.d_h = d_h; s.d_w = d_w;
+  s.ntens = k_only ? 1 : 2;
+  s.turn = turn;
+  const long long want = (s.ntok + kRopeTokens - 1) / kRopeTokens;
+  const long long cap = (long long)sm_count() * 8;
+  const unsigned grid = (unsigned)(want < cap ? want : cap);
+  rope3d_kernel<<<grid, kRopeThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+      static_cast<const __nv_bfloat16*>(q_in), static_cast<const __nv_bfloat16*>(k_in),
+      static_cast<__nv_bfloat16*>(q_out), static_cast<__nv_bfloat16*>(k_out), s, (double)theta);
+  return last_launch_status();
+}
+
+// CTAs that share a pair of query blocks: as many as leave no SM of a full
+// wave idle, in the powers of two that tile a GPC's SMs (a cluster of 8 needs 8
+// free SMs of one GPC; 128 of the 148 can hold such clusters at once), each
+// with two key blocks or more to choose from.
+int sparse_splits(long long units, int nkb) {
+  int s = 8;
+  while (s > 1 && (units * s > 128 || nkb < 2 * s)) s /= 2;
+  return s;
+}
+
+template <int D>
+int launch_block_sparse(const void* q, const void* k, const void* v, void* o, float* lse, const void* blocks, int B,
+                        int Lq, int Lk, int heads, float scale, cudaStream_t stream) {
+  using C = SparseCfg<D>;
+  static bool done[kMaxDevices] = {}, done_split[kMaxDevices] = {};
+  static std::mutex mu;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ensure_smem(attn_fwd_tcgen05_sparse_kernel<D, false>, C::SMEM_BYTES, done) ||
+        !ensure_smem(attn_fwd_tcgen05_sparse_kernel<D, true>, C::SMEM_BYTES, done_split))
+      return VDIT_ERR_CUDA;
+  }
+  const long long tok = (long long)heads * D;
+  CUtensorMap mq, mk, mv, mo;
+  if (!make_qkv_map(&mq, q, D, heads, 1, Lq, B, tok, tok, tok * Lq) ||
+      !make_qkv_map(&mk, k, D, heads, 1, Lk, B, tok, tok, tok * Lk) ||
+      !make_qkv_map(&mv, v, D, heads, 1, Lk, B, tok, tok, tok * Lk) ||
+      !make_qkv_map(&mo, o, D, heads, 1, Lq, B, tok, tok, tok * Lq))
+    return VDIT_ERR_CUDA;
+  SparseParams p{};
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.blocks = static_cast<const uint8_t*>(blocks);
+  p.Lq = Lq; p.Lk = Lk; p.heads = heads;
+  p.nqb = sparse_blocks(Lq); p.nkb = sparse_blocks(Lk);
+  p.n_pairs = (p.nqb + 1) / 2;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const long long units = (long long)B * heads * p.n_pairs;
+  if (units > 0x7fffffffLL) return VDIT_ERR_SHAPE;
+  p.splits = sparse_splits(units, p.nkb);
+  if (p.splits == 1) {
+    attn_fwd_tcgen05_sparse_kernel<D, false><<<(unsigned)units, C::THREADS, C::SMEM_BYTES, stream>>>(mq, mk, mv, mo, p);
+    return last_launch_status();
+  }
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)p.splits;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(units * p.splits));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attn_fwd_tcgen05_sparse_kernel<D, true>, mq, mk, mv, mo, p) != cudaSuccess) {
+    cudaGetLastError();
+    return VDIT_ERR_CUDA;
+  }
+  return last_launch_status();
+}
+
+template <int D>
+int launch_block_sparse_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                            const void* d_o, const void* blocks, void* dq, void* dk, void* dv, float* stats, int B,
+                            int Lq, int Lk, int heads, float scale, cudaStream_t stream) {
+  using C = SparseBwdCfg<D>;
+  static bool done_q[kMaxDevices] = {}, done_kv[kMaxDevices] = {};
+  static std::mutex mu;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ensure_smem(grad_attn_fwd_tcgen05_sparse_dq_kernel<D>, C::DQ_SMEM, done_q) ||
+        !ensure_smem(grad_attn_fwd_tcgen05_sparse_dkv_kernel<D>, C::DKV_SMEM, done_kv))
+      return VDIT_ERR_CUDA;
+  }
+  const long long tok = (long long)heads * D;
+  CUtensorMap mq, mk, mv, mg, mdq, mdk, mdv;
+  const struct { CUtensorMap* map; const void* at; int L; } maps[7] = {
+      {&mq, q, Lq}, {&mk, k, Lk}, {&mv, v, Lk}, {&mg, d_o, Lq}, {&mdq, dq, Lq}, {&mdk, dk, Lk}, {&mdv, dv, Lk}};
+  for (const auto& m : maps)
+    if (!make_qkv_map(m.map, m.at, D, heads, 1, m.L, B, tok, tok, tok * m.L)) return VDIT_ERR_CUDA;
+  SparseBwdParams p{};
+  p.o = static_cast<const __nv_bfloat16*>(o);
+  p.d_o = static_cast<const __nv_bfloat16*>(d_o);
+  p.lse = lse;
+  p.stats = stats;
+  p.blocks = static_cast<const uint8_t*>(blocks);
+  p.Lq = Lq; p.Lk = Lk; p.heads = heads;
+  p.nqb = sparse_blocks(Lq); p.nkb = sparse_blocks(Lk);
+  p.stats_n = (long long)B * heads * p.nqb * 128;
+  p.scale = scale;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const long long gq = (long long)B * heads * p.nqb, gk = (long long)B * heads * p.nkb;
+  if (gq > 0x7fffffffLL || gk > 0x7fffffffLL) return VDIT_ERR_SHAPE;
+  grad_attn_fwd_tcgen05_sparse_dq_kernel<D><<<(unsigned)gq, C::THREADS, C::DQ_SMEM, stream>>>(mq, mk, mv, mg, mdq, p);
+  const int rc = last_launch_status();
+  if (rc != VDIT_OK) return rc;
+  grad_attn_fwd_tcgen05_sparse_dkv_kernel<D><<<(unsigned)gk, C::THREADS, C::DKV_SMEM, stream>>>(mq, mk, mv, mg, mdk,
+                                                                                             mdv, p);
+  return last_launch_status();
+}
+
 }  // namespace
+
+namespace vdit {
+
+const unsigned int* watchdog_flag() {
+  static const unsigned int* at[kMaxDevices] = {};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  std::lock_guard<std::mutex> lock(mu);
+  if (at[dev] == nullptr) {
+    void* a = nullptr;
+    if (cudaGetSymbolAddress(&a, g_watchdog) != cudaSuccess) return nullptr;
+    at[dev] = static_cast<const unsigned int*>(a);
+  }
+  return at[dev];
+}
+
+}  // namespace vdit
 
 extern "C" {
 
@@ -454,30 +608,12 @@ int vdit_patch_embed_3d(const float* latent, const void* weight, const float* bi
 
 int vdit_rope_3d(const void* q_in, const void* k_in, void* q_out, void* k_out, int B, int Tg, int Hg, int Wg,
                  int heads, int head_dim, int d_t, int d_h, int d_w, float theta, vdit_stream_t stream) {
-  const bool k_only = q_in == nullptr && q_out == nullptr;
-  if (k_only) { q_in = k_in; q_out = k_out; }
-  if (!q_in || !k_in || !q_out || !k_out) return VDIT_ERR_NULL;
-  if (B <= 0 || Tg <= 0 || Hg <= 0 || Wg <= 0 || heads <= 0 || head_dim <= 0) return VDIT_ERR_SHAPE;
-  if (d_t < 0 || d_h < 0 || d_w < 0 || (d_t | d_h | d_w) & 1 || d_t + d_h + d_w != head_dim) return VDIT_ERR_SHAPE;
-  if (!(theta > 0.f) || !std::isfinite(theta)) return VDIT_ERR_SHAPE;
-  if (head_dim % 8 != 0 || head_dim / 2 > kRopeMaxPairs) return VDIT_ERR_UNSUPPORTED;
-  if (!aligned16(q_in) || !aligned16(k_in) || !aligned16(q_out) || !aligned16(k_out)) return VDIT_ERR_ALIGN;
-  const long long L = (long long)Tg * Hg * Wg;
-  if (L > 0x7fffffffLL || (double)B * (double)L * heads * head_dim > 4.0e18) return VDIT_ERR_SHAPE;
-  RopeShape s;
-  s.ntok = (long long)B * L;
-  s.L = (int)L; s.Hg = Hg; s.Wg = Wg;
-  s.heads = heads; s.D = head_dim;
-  s.pt_end = d_t / 2; s.ph_end = (d_t + d_h) / 2;
-  s.d_t = d_t; s.d_h = d_h; s.d_w = d_w;
-  s.ntens = k_only ? 1 : 2;
-  const long long want = (s.ntok + kRopeTokens - 1) / kRopeTokens;
-  const long long cap = (long long)sm_count() * 8;
-  const unsigned grid = (unsigned)(want < cap ? want : cap);
-  rope3d_kernel<<<grid, kRopeThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      static_cast<const __nv_bfloat16*>(q_in), static_cast<const __nv_bfloat16*>(k_in),
-      static_cast<__nv_bfloat16*>(q_out), static_cast<__nv_bfloat16*>(k_out), s, (double)theta);
-  return last_launch_status();
+  return rope_pass(q_in, k_in, q_out, k_out, B, Tg, Hg, Wg, heads, head_dim, d_t, d_h, d_w, theta, 1.f, stream);
+}
+
+int vdit_rope_3d_bwd(const void* gq, const void* gk, void* dq, void* dk, int B, int Tg, int Hg, int Wg, int heads,
+                     int head_dim, int d_t, int d_h, int d_w, float theta, vdit_stream_t stream) {
+  return rope_pass(gq, gk, dq, dk, B, Tg, Hg, Wg, heads, head_dim, d_t, d_h, d_w, theta, -1.f, stream);
 }
 
 int vdit_qk_norm_rope_3d(const void* q_in, const void* k_in, void* q_out, void* k_out, const float* wq,
@@ -638,6 +774,130 @@ int vdit_attn_divided_time(const void* q, const void* k, const void* v, void* o,
     case 128: return dispatch_time_short<128>(q, k, v, p, st);
     default: return VDIT_ERR_UNSUPPORTED;
   }
+}
+
+int vdit_attn_block_sparse(const void* q, const void* k, const void* v, const void* blocks, void* o, float* lse, int B,
+                           int Lq, int Lk, int heads, int head_dim, float scale, vdit_stream_t stream) {
+  if (!blocks) return VDIT_ERR_NULL;
+  int rc = check_attn_args(q, k, v, o, lse, B, Lq, heads, head_dim);
+  if (rc == VDIT_OK) rc = check_attn_args(q, k, v, o, lse, B, Lk, heads, head_dim);
+  if (rc != VDIT_OK) return rc;
+  if (sparse_blocks(Lk) > kSparseMaxBlocks) return VDIT_ERR_UNSUPPORTED;
+  const float sc = resolve_scale(scale, head_dim);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  switch (head_dim) {
+    case 32: return launch_block_sparse<32>(q, k, v, o, lse, blocks, B, Lq, Lk, heads, sc, st);
+    case 64: return launch_block_sparse<64>(q, k, v, o, lse, blocks, B, Lq, Lk, heads, sc, st);
+    default: return launch_block_sparse<128>(q, k, v, o, lse, blocks, B, Lq, Lk, heads, sc, st);
+  }
+}
+
+long long vdit_attn_block_sparse_bwd_workspace(int B, int Lq, int heads) {
+  if (B <= 0 || Lq <= 0 || heads <= 0 || (double)B * heads * ((double)Lq + 128.) > 1.0e17) return -1;
+  return 2LL * B * heads * sparse_blocks(Lq) * 128 * (long long)sizeof(float);
+}
+
+int vdit_attn_block_sparse_bwd(const void* q, const void* k, const void* v, const void* blocks, const void* o,
+                               const float* lse, const void* d_o, void* dq, void* dk, void* dv, void* workspace,
+                               int B, int Lq, int Lk, int heads, int head_dim, float scale, vdit_stream_t stream) {
+  if (!blocks || !o || !lse || !d_o || !dq || !dk || !dv || !workspace) return VDIT_ERR_NULL;
+  int rc = check_attn_args(q, k, v, dq, lse, B, Lq, heads, head_dim);
+  if (rc == VDIT_OK) rc = check_attn_args(q, k, v, dk, lse, B, Lk, heads, head_dim);
+  if (rc != VDIT_OK) return rc;
+  if (!aligned16(o) || !aligned16(d_o) || !aligned16(dv) || !aligned16(workspace)) return VDIT_ERR_ALIGN;
+  if (sparse_blocks(Lk) > kSparseMaxBlocks || sparse_blocks(Lq) > kSparseMaxBlocks) return VDIT_ERR_UNSUPPORTED;
+  const float sc = resolve_scale(scale, head_dim);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  float* stats = static_cast<float*>(workspace);
+  switch (head_dim) {
+    case 32:
+      return launch_block_sparse_bwd<32>(q, k, v, o, lse, d_o, blocks, dq, dk, dv, stats, B, Lq, Lk, heads, sc, st);
+    case 64:
+      return launch_block_sparse_bwd<64>(q, k, v, o, lse, d_o, blocks, dq, dk, dv, stats, B, Lq, Lk, heads, sc, st);
+    default:
+      return launch_block_sparse_bwd<128>(q, k, v, o, lse, d_o, blocks, dq, dk, dv, stats, B, Lq, Lk, heads, sc, st);
+  }
+}
+
+long long vdit_qk_norm_rope_3d_bwd_workspace(int norm_group) {
+  return norm_group > 0 ? 2LL * kNormBwdMaxCtas * norm_group * (long long)sizeof(float) : -1;
+}
+
+int vdit_qk_norm_rope_3d_bwd(const void* q, const void* k, const void* gq, const void* gk, void* dq, void* dk,
+                             const float* wq, const float* wk, float* dwq, float* dwk, void* workspace,
+                             int norm_group, float eps, int B, int Tg, int Hg, int Wg, int heads, int head_dim,
+                             int d_t, int d_h, int d_w, float theta, vdit_stream_t stream) {
+  const bool k_only = q == nullptr && gq == nullptr && dq == nullptr;
+  if (k_only) { q = k; gq = gk; dq = dk; }
+  if (!q || !k || !gq || !gk || !dq || !dk) return VDIT_ERR_NULL;
+  const bool weights = dwk != nullptr || (dwq != nullptr && !k_only);
+  if (weights && !workspace) return VDIT_ERR_NULL;
+  int rc = check_rope_shape(Tg, Hg, Wg, head_dim, d_t, d_h, d_w, theta);
+  if (rc != VDIT_OK) return rc;
+  if (B <= 0 || heads <= 0) return VDIT_ERR_SHAPE;
+  const long long width = (long long)heads * head_dim;
+  if (norm_group <= 0 || width % norm_group != 0 || !(eps >= 0.f) || !std::isfinite(eps)) return VDIT_ERR_SHAPE;
+  if (head_dim % 8 != 0 || head_dim / 2 > kRopeMaxPairs || norm_group % 8 != 0) return VDIT_ERR_UNSUPPORTED;
+  const bool wide = norm_group == width;               // one group: the token's whole vector
+  if (!wide && 32 % (norm_group / 8) != 0) return VDIT_ERR_UNSUPPORTED;
+  if (width > 256LL * 8 * kNormBwdVecs) return VDIT_ERR_UNSUPPORTED;
+  const void* ptrs[] = {q, k, gq, gk, dq, dk, wq, wk, workspace};
+  for (const void* x : ptrs)
+    if (x && !aligned16(x)) return VDIT_ERR_ALIGN;
+  const long long tab = rope_table_entries(Tg, Hg, Wg, d_t, d_h, d_w);
+  if (tab > kNormMaxTable) return VDIT_ERR_UNSUPPORTED;
+  RopeShape s;
+  s.L = Tg * Hg * Wg; s.Hg = Hg; s.Wg = Wg;
+  s.ntok = (long long)B * s.L;
+  if ((double)s.ntok * (double)width > 4.0e18) return VDIT_ERR_SHAPE;
+  s.heads = heads; s.D = head_dim;
+  s.pt_end = d_t / 2; s.ph_end = (d_t + d_h) / 2;
+  s.d_t = d_t; s.d_h = d_h; s.d_w = d_w;
+  s.ntens = k_only ? 1 : 2;
+  NormBwdParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.gq = static_cast<const __nv_bfloat16*>(gq);
+  p.gk = static_cast<const __nv_bfloat16*>(gk);
+  p.dq = static_cast<__nv_bfloat16*>(dq);
+  p.dk = static_cast<__nv_bfloat16*>(dk);
+  p.wq = wq; p.wk = wk;
+  p.parts = weights ? static_cast<float*>(workspace) : nullptr;
+  p.group = norm_group;
+  p.eps = eps;
+  p.theta = (double)theta;
+  // the ring (x and g rows of `stages` tokens) and the per-axis (cos, sin)
+  // tables, in half of an SM's shared memory where two stages fit there
+  constexpr long long kHalf = 110 * 1024, kMost = 224 * 1024;
+  const long long stage = 4 * width;
+  long long stages = (kHalf - tab * 8) / stage;
+  if (stages < 2) stages = (kMost - tab * 8) / stage;
+  if (stages > kNormBwdMaxStages) stages = kNormBwdMaxStages;
+  p.stages = (int)stages;                              // at least 4: 160 KB over a 32 KB stage
+  long long smem = stages * stage + tab * 8;
+  if (smem < 256 * 8 * 4) smem = 256 * 8 * 4;          // the weight gradient's threads meet in 8 KB
+  {
+    static bool done_n[kMaxDevices] = {}, done_w[kMaxDevices] = {};
+    static std::mutex mu;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ensure_smem(bwd_qk_norm_rope3d_kernel<false>, (int)kMost, done_n) ||
+        !ensure_smem(bwd_qk_norm_rope3d_kernel<true>, (int)kMost, done_w))
+      return VDIT_ERR_CUDA;
+  }
+  long long ctas = sm_count();
+  if (ctas > kNormBwdMaxCtas) ctas = kNormBwdMaxCtas;
+  if (ctas > s.ntok) ctas = s.ntok;
+  const dim3 grid((unsigned)ctas, (unsigned)s.ntens);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (wide)
+    bwd_qk_norm_rope3d_kernel<true><<<grid, kNormBwdThreads, (size_t)smem, st>>>(p, s);
+  else
+    bwd_qk_norm_rope3d_kernel<false><<<grid, kNormBwdThreads, (size_t)smem, st>>>(p, s);
+  rc = last_launch_status();
+  if (rc != VDIT_OK || !weights) return rc;
+  bwd_weights_qk_norm_rope3d_kernel<<<dim3((unsigned)((norm_group + 31) / 32), 2), 256, 0, st>>>(
+      p.parts, k_only ? nullptr : dwq, dwk, norm_group, (int)ctas);
+  return last_launch_status();
 }
 
 }  // extern "C"
