@@ -35,7 +35,17 @@ __device__ __forceinline__ bool tripped(const unsigned int* flag) {
 }
 
 // Means of every 128-token block of Q (blockIdx.x < nqb) and K: a CTA takes 256
-// channels of one block, a thread 8 channels of every 8th token.
+// channels of one block, a thread 8 channels of every 8th token.  bound by the
+// bytes of Q and K; a conversion instruction to float64 per value would take
+// longer than they do (16 per clock and SM), so a bfloat16's bits are moved into
+// a float64's high word as they are: exponent field e stands for 2^(e - 1023)
+// there and 2^(e - 127) in the bfloat16, denormals alike, so the float64 is the
+// value times 2^-896, and the sum is scaled back once.  Exponent 255 (infinities
+// and NaN) would not survive: a thread that meets one sums again by conversions.
+__device__ __forceinline__ double bits_to_double(uint32_t f32_bits) {
+  return __hiloint2double(((int)f32_bits >> 3) & 0x8fffffff, 0);
+}
+
 __global__ void __launch_bounds__(256) block_means_kernel(const __nv_bfloat16* __restrict__ q,
                                                           const __nv_bfloat16* __restrict__ k, double* qm, double* km,
                                                           SelectShape s, const unsigned int* flag) {
@@ -52,14 +62,40 @@ __global__ void __launch_bounds__(256) block_means_kernel(const __nv_bfloat16* _
   double a[8] = {0., 0., 0., 0., 0., 0., 0., 0.};
   if (c0 < width) {
     const __nv_bfloat16* src = (is_q ? q : k) + ((long long)b * L + (long long)blk * kBlock) * width + c0;
-#pragma unroll 4
-    for (int r = sub; r < rows; r += 8) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + (long long)r * width));
+    uint32_t most = 0u;                                  // the largest magnitudes met, as 16-bit halves
+    auto add = [&](const uint4& v) {
       const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        a[2 * m] += (double)__uint_as_float(u[m] << 16);
-        a[2 * m + 1] += (double)__uint_as_float(u[m] & 0xffff0000u);
+        a[2 * m] += bits_to_double(u[m] << 16);
+        a[2 * m + 1] += bits_to_double(u[m] & 0xffff0000u);
+        most = __vmaxu2(most, u[m] & 0x7fff7fffu);
+      }
+    };
+    if (rows == kBlock) {                                // a whole block: 16 tokens, 8 loads in flight
+#pragma unroll
+      for (int r0 = 0; r0 < 16; r0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          v[r] = __ldcs(reinterpret_cast<const uint4*>(src + (long long)(sub + 8 * (r0 + r)) * width));
+#pragma unroll
+        for (int r = 0; r < 8; ++r) add(v[r]);
+      }
+    } else {
+      for (int r = sub; r < rows; r += 8) add(__ldcs(reinterpret_cast<const uint4*>(src + (long long)r * width)));
+    }
+    if ((most & 0xffffu) >= 0x7f80u || (most >> 16) >= 0x7f80u) {
+#pragma unroll
+      for (int m = 0; m < 8; ++m) a[m] = 0.;
+      for (int r = sub; r < rows; r += 8) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + (long long)r * width));
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          a[2 * m] += (double)__uint_as_float(u[m] << 16) * 0x1p-896;
+          a[2 * m + 1] += (double)__uint_as_float(u[m] & 0xffff0000u) * 0x1p-896;
+        }
       }
     }
   }
@@ -73,7 +109,7 @@ __global__ void __launch_bounds__(256) block_means_kernel(const __nv_bfloat16* _
 #pragma unroll
     for (int i = 0; i < 8; ++i) t += part[i][threadIdx.x >> 3][threadIdx.x & 7];
     const int h = c / s.D, d = c - h * s.D;
-    (is_q ? qm : km)[(((long long)b * s.heads + h) * n + blk) * s.D + d] = t / (double)rows;
+    (is_q ? qm : km)[(((long long)b * s.heads + h) * n + blk) * s.D + d] = t * 0x1p896 / (double)rows;
   }
 }
 
@@ -84,18 +120,20 @@ __device__ __forceinline__ unsigned long long order_key(double x) {
   return v < 0 ? ~(unsigned long long)v : (unsigned long long)v | 0x8000000000000000ull;
 }
 
-// Scores of 64 query blocks x 64 key blocks of one head, 4 x 4 per thread.
-__global__ void __launch_bounds__(256) block_scores_kernel(const double* __restrict__ qm,
-                                                           const double* __restrict__ km, unsigned long long* keys,
-                                                           SelectShape s, const unsigned int* flag) {
+// Scores of 64 query blocks x 64 key blocks of one head: 64 threads, 8 x 8 each
+// (two shared-memory loads per eight multiply-adds).  Bound by the float64 units.
+__global__ void __launch_bounds__(64) block_scores_kernel(const double* __restrict__ qm, const double* __restrict__ km,
+                                                          unsigned long long* keys, SelectShape s,
+                                                          const unsigned int* flag) {
   __shared__ double sq[16][65], sk[16][65];
   if (tripped(flag)) return;
   const long long bh = blockIdx.z;
   const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  double acc[4][4] = {};
+  const int ty = threadIdx.x >> 3, tx = threadIdx.x & 7;
+  double acc[8][8] = {};
   for (int d0 = 0; d0 < s.D; d0 += 16) {
-    for (int e = threadIdx.x; e < 64 * 16; e += 256) {
+#pragma unroll 8
+    for (int e = threadIdx.x; e < 64 * 16; e += 64) {
       const int r = e >> 4, d = e & 15;
       sq[d][r] = i0 + r < s.nqb ? qm[(bh * s.nqb + i0 + r) * s.D + d0 + d] : 0.;
       sk[d][r] = j0 + r < s.nkb ? km[(bh * s.nkb + j0 + r) * s.D + d0 + d] : 0.;
@@ -103,26 +141,32 @@ __global__ void __launch_bounds__(256) block_scores_kernel(const double* __restr
     __syncthreads();
 #pragma unroll
     for (int d = 0; d < 16; ++d) {
-      double x[4], y[4];
+      double x[8], y[8];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) { x[m] = sq[d][ty + 16 * m]; y[m] = sk[d][tx + 16 * m]; }
+      for (int m = 0; m < 8; ++m) { x[m] = sq[d][ty + 8 * m]; y[m] = sk[d][tx + 8 * m]; }
 #pragma unroll
-      for (int m = 0; m < 4; ++m)
+      for (int m = 0; m < 8; ++m)
 #pragma unroll
-        for (int n = 0; n < 4; ++n) acc[m][n] = fma(x[m], y[n], acc[m][n]);
+        for (int n = 0; n < 8; ++n) acc[m][n] = fma(x[m], y[n], acc[m][n]);
     }
     __syncthreads();
   }
 #pragma unroll
-  for (int m = 0; m < 4; ++m)
+  for (int m = 0; m < 8; ++m)
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const int i = i0 + ty + 16 * m, j = j0 + tx + 16 * n;
+    for (int n = 0; n < 8; ++n) {
+      const int i = i0 + ty + 8 * m, j = j0 + tx + 8 * n;
       if (i < s.nqb && j < s.nkb) keys[(bh * s.nqb + i) * s.nkb + j] = order_key(acc[m][n]);
     }
 }
 
-// One warp per row: the top_k-th highest key, bit by bit; then the row's marks.
+// One warp per row: a threshold t with exactly top_k keys at or above it, bit by
+// bit from the first bit in which the row's keys differ (the search ends as soon
+// as the count fits: some 20 of 64 bits); then the row's marks.  Only where keys
+// are equal can the search end with more than top_k at or above t; of those equal
+// to t the first ones are marked.  N > 0: a row of at most 32 N keys is held in
+// registers; N = 0: longer rows are read again for each bit.
+template <int N>
 __global__ void __launch_bounds__(256) block_pick_kernel(const unsigned long long* __restrict__ keys,
                                                          unsigned char* blocks, long long rows, SelectShape s,
                                                          const unsigned int* flag) {
@@ -131,25 +175,64 @@ __global__ void __launch_bounds__(256) block_pick_kernel(const unsigned long lon
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
   const unsigned long long* key = keys + row * s.nkb;
-  unsigned long long t = 0ull;
-  for (int bit = 63; bit >= 0; --bit) {
-    const unsigned long long cand = t | (1ull << bit);
+  unsigned long long held[N > 0 ? N : 1];
+#pragma unroll
+  for (int i = 0; i < N; ++i) held[i] = i * 32 + lane < s.nkb ? __ldcs(key + i * 32 + lane) : 0ull;
+  auto each = [&](auto f) {                              // f(key) over this lane's keys
+    if constexpr (N > 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i * 32 + lane < s.nkb) f(held[i]);
+    } else {
+      for (int j = lane; j < s.nkb; j += 32) f(key[j]);
+    }
+  };
+  // the bits all keys of the row share, by the high words' extremes
+  uint32_t lo = 0xffffffffu, hi = 0u;
+  each([&](unsigned long long x) {
+    const uint32_t h = (uint32_t)(x >> 32);
+    lo = min(lo, h);
+    hi = max(hi, h);
+  });
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  uint32_t t = 0u;                                       // the threshold's high word
+  int above = s.nkb;                                     // keys at or above the threshold
+  const int top = 31 - __clz((int)(lo ^ hi));            // -1: all high words are equal
+  t = top < 0 ? hi : (top < 31 ? hi & ~((2u << top) - 1u) : 0u);
+  for (int bit = top; bit >= 0 && above != s.top_k; --bit) {
+    const uint32_t cand = t | (1u << bit);
     int n = 0;
-    for (int j = lane; j < s.nkb; j += 32) n += key[j] >= cand;
+    each([&](unsigned long long x) { n += (uint32_t)(x >> 32) >= cand; });
     n = __reduce_add_sync(0xffffffffu, n);
-    if (n >= s.top_k) t = cand;
+    if (n >= s.top_k) { t = cand; above = n; }
   }
-  int above = 0;
-  for (int j = lane; j < s.nkb; j += 32) above += key[j] > t;
-  int ties = s.top_k - (int)__reduce_add_sync(0xffffffffu, above);   // of the keys equal to t, the first so many
-  for (int j0 = 0; j0 < s.nkb; j0 += 32) {
-    const int j = j0 + lane;
-    const unsigned long long x = j < s.nkb ? key[j] : 0ull;
-    const bool eq = j < s.nkb && x == t;
+  unsigned long long thr = (unsigned long long)t << 32;
+  for (int bit = 31; bit >= 0 && above != s.top_k; --bit) {
+    const unsigned long long cand = thr | (1ull << bit);
+    int n = 0;
+    each([&](unsigned long long x) { n += x >= cand; });
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (n >= s.top_k) { thr = cand; above = n; }
+  }
+  int ties = s.nkb;                                      // marks left for keys equal to thr
+  if (above != s.top_k) {
+    int n = 0;
+    each([&](unsigned long long x) { n += x > thr; });
+    ties = s.top_k - (int)__reduce_add_sync(0xffffffffu, n);
+  }
+  auto mark = [&](int j, unsigned long long x) {
+    const bool eq = j < s.nkb && x == thr;
     const unsigned int eqs = __ballot_sync(0xffffffffu, eq);
-    const bool on = j < s.nkb && (x > t || (eq && __popc(eqs & ((1u << lane) - 1u)) < ties));
+    const bool on = x > thr || (eq && __popc(eqs & ((1u << lane) - 1u)) < ties);
     ties -= min(ties, __popc(eqs));
     if (j < s.nkb) blocks[row * s.nkb + j] = on ? 1 : 0;
+  };
+  if constexpr (N > 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) mark(i * 32 + lane, held[i]);
+  } else {
+    for (int j0 = 0; j0 < s.nkb; j0 += 32) mark(j0 + lane, j0 + lane < s.nkb ? key[j0 + lane] : 0ull);
   }
 }
 
@@ -198,9 +281,13 @@ int vdit_attn_select_blocks(const void* q, const void* k, void* blocks, void* wo
   unsigned long long* keys = reinterpret_cast<unsigned long long*>(qm + mean_count(s));
   block_means_kernel<<<dim3((unsigned)(s.nqb + s.nkb), (unsigned)chunks, (unsigned)B), 256, 0, st>>>(
       static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k), qm, km, s, flag);
-  block_scores_kernel<<<dim3((unsigned)kt, (unsigned)qt, (unsigned)bh), 256, 0, st>>>(qm, km, keys, s, flag);
-  block_pick_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(keys, static_cast<unsigned char*>(blocks), rows, s,
-                                                               flag);
+  block_scores_kernel<<<dim3((unsigned)kt, (unsigned)qt, (unsigned)bh), 64, 0, st>>>(qm, km, keys, s, flag);
+  unsigned char* out = static_cast<unsigned char*>(blocks);
+  const unsigned picks = (unsigned)((rows + 7) / 8);
+  if (s.nkb <= 128) block_pick_kernel<4><<<picks, 256, 0, st>>>(keys, out, rows, s, flag);
+  else if (s.nkb <= 256) block_pick_kernel<8><<<picks, 256, 0, st>>>(keys, out, rows, s, flag);
+  else if (s.nkb <= 640) block_pick_kernel<20><<<picks, 256, 0, st>>>(keys, out, rows, s, flag);
+  else block_pick_kernel<0><<<picks, 256, 0, st>>>(keys, out, rows, s, flag);
   return cudaGetLastError() == cudaSuccess ? VDIT_OK : VDIT_ERR_CUDA;
 }
 

@@ -414,6 +414,24 @@ int launch_block_sparse_bwd(const void* q, const void* k, const void* v, const v
   return last_launch_status();
 }
 
+template <int V>
+int launch_norm_rope_bwd(bool wide, const NormBwdParams& p, const RopeShape& s, dim3 grid, int threads, int smem,
+                         int smem_limit, cudaStream_t stream) {
+  static bool done_n[kMaxDevices] = {}, done_w[kMaxDevices] = {};
+  static std::mutex mu;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ensure_smem(bwd_qk_norm_rope3d_kernel<false, V>, smem_limit, done_n) ||
+        !ensure_smem(bwd_qk_norm_rope3d_kernel<true, V>, smem_limit, done_w))
+      return VDIT_ERR_CUDA;
+  }
+  if (wide)
+    bwd_qk_norm_rope3d_kernel<true, V><<<grid, threads, smem, stream>>>(p, s);
+  else
+    bwd_qk_norm_rope3d_kernel<false, V><<<grid, threads, smem, stream>>>(p, s);
+  return last_launch_status();
+}
+
 }  // namespace
 
 namespace vdit {
@@ -840,7 +858,7 @@ int vdit_qk_norm_rope_3d_bwd(const void* q, const void* k, const void* gq, const
   if (head_dim % 8 != 0 || head_dim / 2 > kRopeMaxPairs || norm_group % 8 != 0) return VDIT_ERR_UNSUPPORTED;
   const bool wide = norm_group == width;               // one group: the token's whole vector
   if (!wide && 32 % (norm_group / 8) != 0) return VDIT_ERR_UNSUPPORTED;
-  if (width > 256LL * 8 * kNormBwdVecs) return VDIT_ERR_UNSUPPORTED;
+  if (width > 8192) return VDIT_ERR_UNSUPPORTED;
   const void* ptrs[] = {q, k, gq, gk, dq, dk, wq, wk, workspace};
   for (const void* x : ptrs)
     if (x && !aligned16(x)) return VDIT_ERR_ALIGN;
@@ -866,34 +884,41 @@ int vdit_qk_norm_rope_3d_bwd(const void* q, const void* k, const void* gq, const
   p.group = norm_group;
   p.eps = eps;
   p.theta = (double)theta;
-  // the ring (x and g rows of `stages` tokens) and the per-axis (cos, sin)
-  // tables, in half of an SM's shared memory where two stages fit there
-  constexpr long long kHalf = 110 * 1024, kMost = 224 * 1024;
-  const long long stage = 4 * width;
-  long long stages = (kHalf - tab * 8) / stage;
-  if (stages < 2) stages = (kMost - tab * 8) / stage;
-  if (stages > kNormBwdMaxStages) stages = kNormBwdMaxStages;
-  p.stages = (int)stages;                              // at least 4: 160 KB over a 32 KB stage
-  long long smem = stages * stage + tab * 8;
-  if (smem < 256 * 8 * 4) smem = 256 * 8 * 4;          // the weight gradient's threads meet in 8 KB
-  {
-    static bool done_n[kMaxDevices] = {}, done_w[kMaxDevices] = {};
-    static std::mutex mu;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!ensure_smem(bwd_qk_norm_rope3d_kernel<false>, (int)kMost, done_n) ||
-        !ensure_smem(bwd_qk_norm_rope3d_kernel<true>, (int)kMost, done_w))
-      return VDIT_ERR_CUDA;
+  // V vectors per thread, `warps` warps per token, `groups` tokens per CTA: as
+  // few vectors per thread as 320 threads cover, then as many tokens as 8 warps
+  const int nv = (int)(width / 8);
+  const int V = (nv + kNormBwdThreads - 1) / kNormBwdThreads;
+  p.warps = (nv + 32 * V - 1) / (32 * V);
+  p.groups = p.warps >= 8 ? 1 : 8 / p.warps;
+  const int threads = 32 * p.warps * p.groups;
+  // Shared memory: the ring (x and g rows of `stages` chunks), two chunks' pairs
+  // and the per-axis tables.  Three CTAs (V = 1) or two share an SM where two
+  // stages each fit, else one takes it.
+  constexpr long long kMost = 224 * 1024;
+  const long long stage = 4 * width * p.groups;
+  const long long fixed = 2LL * p.groups * head_dim / 2 * 8 + tab * 8;
+  int per_sm = V == 1 ? 3 : 2;
+  long long stages = (kMost / per_sm - 2048 - fixed) / stage;
+  while (stages < 2 && per_sm > 1) {
+    --per_sm;
+    stages = (kMost / per_sm - 2048 - fixed) / stage;
   }
-  long long ctas = sm_count();
+  if (stages > kNormBwdMaxStages) stages = kNormBwdMaxStages;
+  p.stages = (int)stages;                              // at least 4: 156 KB over a 32 KB stage
+  long long smem = stages * stage + fixed;
+  if (smem < threads * 32) smem = threads * 32;        // the threads' parts of the weight gradient meet there
+  const long long chunks = (s.ntok + p.groups - 1) / p.groups;
+  // half of the CTAs for each tensor; K alone takes no more, so that its weight
+  // gradient is summed in the same order as beside Q
+  long long ctas = (long long)sm_count() * per_sm / 2;
   if (ctas > kNormBwdMaxCtas) ctas = kNormBwdMaxCtas;
-  if (ctas > s.ntok) ctas = s.ntok;
+  if (ctas > chunks) ctas = chunks;
   const dim3 grid((unsigned)ctas, (unsigned)s.ntens);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (wide)
-    bwd_qk_norm_rope3d_kernel<true><<<grid, kNormBwdThreads, (size_t)smem, st>>>(p, s);
-  else
-    bwd_qk_norm_rope3d_kernel<false><<<grid, kNormBwdThreads, (size_t)smem, st>>>(p, s);
-  rc = last_launch_status();
+  rc = V == 1   ? launch_norm_rope_bwd<1>(wide, p, s, grid, threads, (int)smem, (int)kMost, st)
+       : V == 2 ? launch_norm_rope_bwd<2>(wide, p, s, grid, threads, (int)smem, (int)kMost, st)
+       : V == 3 ? launch_norm_rope_bwd<3>(wide, p, s, grid, threads, (int)smem, (int)kMost, st)
+                : launch_norm_rope_bwd<4>(wide, p, s, grid, threads, (int)smem, (int)kMost, st);
   if (rc != VDIT_OK || !weights) return rc;
   bwd_weights_qk_norm_rope3d_kernel<<<dim3((unsigned)((norm_group + 31) / 32), 2), 256, 0, st>>>(
       p.parts, k_only ? nullptr : dwq, dwk, norm_group, (int)ctas);
