@@ -120,34 +120,65 @@ __device__ __forceinline__ unsigned long long order_key(double x) {
   return v < 0 ? ~(unsigned long long)v : (unsigned long long)v | 0x8000000000000000ull;
 }
 
-// Scores of 64 query blocks x 64 key blocks of one head: 64 threads, 8 x 8 each
-// (two shared-memory loads per eight multiply-adds).  Bound by the float64 units.
+// Scores of 64 query blocks x 64 key blocks of one head: 64 threads, 8 x 8 each,
+// the means fetched 16 channels at a time into two buffers with asynchronous
+// copies (rows of 144 bytes: the eight rows a quarter-warp reads 16 bytes of
+// fall into different banks).  Bound by the float64 units.  The ordered scores
+// leave as two arrays of 32-bit words: the second is hardly ever read.
+constexpr int kScoreRow = 18;                            // doubles per staged row: 16 channels and padding
+
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool on) {
+  const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+
 __global__ void __launch_bounds__(64) block_scores_kernel(const double* __restrict__ qm, const double* __restrict__ km,
-                                                          unsigned long long* keys, SelectShape s,
+                                                          uint32_t* hi, uint32_t* lo, SelectShape s,
                                                           const unsigned int* flag) {
-  __shared__ double sq[16][65], sk[16][65];
+  __shared__ __align__(16) double st[2][2][64 * kScoreRow];
   if (tripped(flag)) return;
   const long long bh = blockIdx.z;
   const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
   const int ty = threadIdx.x >> 3, tx = threadIdx.x & 7;
+  auto fetch = [&](int buf, int d0) {                    // 2 x 64 rows x 8 chunks of 16 bytes
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const int r = ty + 8 * (c & 7), which = c >> 3;
+      const int row = (which ? j0 : i0) + r, n = which ? s.nkb : s.nqb;
+      const double* from = (which ? km : qm) + (bh * n + min(row, n - 1)) * s.D + d0 + tx * 2;
+      copy16(&st[buf][which][r * kScoreRow + tx * 2], from, row < n);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
   double acc[8][8] = {};
-  for (int d0 = 0; d0 < s.D; d0 += 16) {
-#pragma unroll 8
-    for (int e = threadIdx.x; e < 64 * 16; e += 64) {
-      const int r = e >> 4, d = e & 15;
-      sq[d][r] = i0 + r < s.nqb ? qm[(bh * s.nqb + i0 + r) * s.D + d0 + d] : 0.;
-      sk[d][r] = j0 + r < s.nkb ? km[(bh * s.nkb + j0 + r) * s.D + d0 + d] : 0.;
+  const int steps = s.D / 16;
+  fetch(0, 0);
+  for (int x = 0; x < steps; ++x) {
+    if (x + 1 < steps) {
+      fetch((x + 1) & 1, (x + 1) * 16);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     __syncthreads();
+    const double* sq = &st[x & 1][0][ty * kScoreRow];
+    const double* sk = &st[x & 1][1][tx * kScoreRow];
 #pragma unroll
-    for (int d = 0; d < 16; ++d) {
-      double x[8], y[8];
+    for (int d = 0; d < 16; d += 2) {
+      double2 q[8], k[8];
 #pragma unroll
-      for (int m = 0; m < 8; ++m) { x[m] = sq[d][ty + 8 * m]; y[m] = sk[d][tx + 8 * m]; }
+      for (int m = 0; m < 8; ++m) {
+        q[m] = *reinterpret_cast<const double2*>(sq + 8 * m * kScoreRow + d);
+        k[m] = *reinterpret_cast<const double2*>(sk + 8 * m * kScoreRow + d);
+      }
 #pragma unroll
       for (int m = 0; m < 8; ++m)
 #pragma unroll
-        for (int n = 0; n < 8; ++n) acc[m][n] = fma(x[m], y[n], acc[m][n]);
+        for (int n = 0; n < 8; ++n) acc[m][n] = fma(q[m].x, k[n].x, acc[m][n]);
+#pragma unroll
+      for (int m = 0; m < 8; ++m)
+#pragma unroll
+        for (int n = 0; n < 8; ++n) acc[m][n] = fma(q[m].y, k[n].y, acc[m][n]);
     }
     __syncthreads();
   }
@@ -156,83 +187,88 @@ __global__ void __launch_bounds__(64) block_scores_kernel(const double* __restri
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
       const int i = i0 + ty + 8 * m, j = j0 + tx + 8 * n;
-      if (i < s.nqb && j < s.nkb) keys[(bh * s.nqb + i) * s.nkb + j] = order_key(acc[m][n]);
+      if (i < s.nqb && j < s.nkb) {
+        const unsigned long long key = order_key(acc[m][n]);
+        hi[(bh * s.nqb + i) * s.nkb + j] = (uint32_t)(key >> 32);
+        lo[(bh * s.nqb + i) * s.nkb + j] = (uint32_t)key;
+      }
     }
 }
 
 // One warp per row: a threshold t with exactly top_k keys at or above it, bit by
-// bit from the first bit in which the row's keys differ (the search ends as soon
-// as the count fits: some 20 of 64 bits); then the row's marks.  Only where keys
-// are equal can the search end with more than top_k at or above t; of those equal
-// to t the first ones are marked.  N > 0: a row of at most 32 N keys is held in
-// registers; N = 0: longer rows are read again for each bit.
+// bit from the first bit in which the row's high words differ; the search ends
+// as soon as the count fits (some 20 of 64 bits).  Only rows whose high words
+// leave it open read the low words.  Only where keys are equal can the search end
+// with more than top_k at or above t: of those equal to t the first ones are
+// marked.  N > 0: the high words of a row of at most 32 N keys are held in
+// registers (zeros past its end, which no threshold of the search counts); N = 0:
+// longer rows are read again for each bit.
 template <int N>
-__global__ void __launch_bounds__(256) block_pick_kernel(const unsigned long long* __restrict__ keys,
-                                                         unsigned char* blocks, long long rows, SelectShape s,
-                                                         const unsigned int* flag) {
+__global__ void __launch_bounds__(256) block_pick_kernel(const uint32_t* __restrict__ hi_words,
+                                                         const uint32_t* __restrict__ lo_words, unsigned char* blocks,
+                                                         long long rows, SelectShape s, const unsigned int* flag) {
   if (tripped(flag)) return;
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
-  const unsigned long long* key = keys + row * s.nkb;
-  unsigned long long held[N > 0 ? N : 1];
+  const uint32_t* hw = hi_words + row * s.nkb;
+  const uint32_t* lw = lo_words + row * s.nkb;
+  unsigned char* out = blocks + row * s.nkb;
+  uint32_t held[N > 0 ? N : 1];
 #pragma unroll
-  for (int i = 0; i < N; ++i) held[i] = i * 32 + lane < s.nkb ? __ldcs(key + i * 32 + lane) : 0ull;
-  auto each = [&](auto f) {                              // f(key) over this lane's keys
+  for (int i = 0; i < N; ++i) held[i] = i * 32 + lane < s.nkb ? __ldcs(hw + i * 32 + lane) : 0u;
+  // the keys of this lane: f(high word, index); `padded`: those past the row's end too, as zeros
+  auto each = [&](bool padded, auto f) {
     if constexpr (N > 0) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (i * 32 + lane < s.nkb) f(held[i]);
+        if (padded || i * 32 + lane < s.nkb) f(held[i], i * 32 + lane);
     } else {
-      for (int j = lane; j < s.nkb; j += 32) f(key[j]);
+      for (int j = lane; j < s.nkb; j += 32) f(hw[j], j);
     }
   };
-  // the bits all keys of the row share, by the high words' extremes
-  uint32_t lo = 0xffffffffu, hi = 0u;
-  each([&](unsigned long long x) {
-    const uint32_t h = (uint32_t)(x >> 32);
-    lo = min(lo, h);
-    hi = max(hi, h);
+  uint32_t least = 0xffffffffu, most = 0u;
+  each(false, [&](uint32_t h, int) {
+    least = min(least, h);
+    most = max(most, h);
   });
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  uint32_t t = 0u;                                       // the threshold's high word
+  least = __reduce_min_sync(0xffffffffu, least);
+  most = __reduce_max_sync(0xffffffffu, most);
   int above = s.nkb;                                     // keys at or above the threshold
-  const int top = 31 - __clz((int)(lo ^ hi));            // -1: all high words are equal
-  t = top < 0 ? hi : (top < 31 ? hi & ~((2u << top) - 1u) : 0u);
+  const int top = 31 - __clz((int)(least ^ most));       // -1: all high words are equal
+  uint32_t t = top < 0 ? most : (top < 31 ? most & ~((2u << top) - 1u) : 0u);
   for (int bit = top; bit >= 0 && above != s.top_k; --bit) {
     const uint32_t cand = t | (1u << bit);
     int n = 0;
-    each([&](unsigned long long x) { n += (uint32_t)(x >> 32) >= cand; });
+    each(true, [&](uint32_t h, int) { n += h >= cand; });
     n = __reduce_add_sync(0xffffffffu, n);
     if (n >= s.top_k) { t = cand; above = n; }
   }
-  unsigned long long thr = (unsigned long long)t << 32;
+  if (above == s.top_k) {
+    each(false, [&](uint32_t h, int j) { out[j] = h >= t ? 1 : 0; });
+    return;
+  }
+  // the low words of the keys whose high word is t decide
+  auto sure = [&](uint32_t h) { return h > t; };
+  uint32_t tl = 0u;
   for (int bit = 31; bit >= 0 && above != s.top_k; --bit) {
-    const unsigned long long cand = thr | (1ull << bit);
+    const uint32_t cand = tl | (1u << bit);
     int n = 0;
-    each([&](unsigned long long x) { n += x >= cand; });
+    each(false, [&](uint32_t h, int j) { n += sure(h) || (h == t && lw[j] >= cand); });
     n = __reduce_add_sync(0xffffffffu, n);
-    if (n >= s.top_k) { thr = cand; above = n; }
+    if (n >= s.top_k) { tl = cand; above = n; }
   }
-  int ties = s.nkb;                                      // marks left for keys equal to thr
-  if (above != s.top_k) {
-    int n = 0;
-    each([&](unsigned long long x) { n += x > thr; });
-    ties = s.top_k - (int)__reduce_add_sync(0xffffffffu, n);
-  }
-  auto mark = [&](int j, unsigned long long x) {
-    const bool eq = j < s.nkb && x == thr;
+  int n = 0;
+  each(false, [&](uint32_t h, int j) { n += sure(h) || (h == t && lw[j] > tl); });
+  int ties = s.top_k - (int)__reduce_add_sync(0xffffffffu, n);   // of the keys equal to (t, tl), the first so many
+  for (int j0 = 0; j0 < s.nkb; j0 += 32) {
+    const int j = j0 + lane;
+    const uint32_t h = j < s.nkb ? hw[j] : 0u, l = j < s.nkb ? lw[j] : 0u;
+    const bool eq = j < s.nkb && h == t && l == tl;
     const unsigned int eqs = __ballot_sync(0xffffffffu, eq);
-    const bool on = x > thr || (eq && __popc(eqs & ((1u << lane) - 1u)) < ties);
+    const bool on = sure(h) || (h == t && l > tl) || (eq && __popc(eqs & ((1u << lane) - 1u)) < ties);
     ties -= min(ties, __popc(eqs));
-    if (j < s.nkb) blocks[row * s.nkb + j] = on ? 1 : 0;
-  };
-  if constexpr (N > 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) mark(i * 32 + lane, held[i]);
-  } else {
-    for (int j0 = 0; j0 < s.nkb; j0 += 32) mark(j0 + lane, j0 + lane < s.nkb ? key[j0 + lane] : 0ull);
+    if (j < s.nkb) out[j] = on ? 1 : 0;
   }
 }
 
@@ -278,16 +314,17 @@ int vdit_attn_select_blocks(const void* q, const void* k, void* blocks, void* wo
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   double* qm = static_cast<double*>(workspace);
   double* km = qm + bh * s.nqb * head_dim;
-  unsigned long long* keys = reinterpret_cast<unsigned long long*>(qm + mean_count(s));
+  uint32_t* hi = reinterpret_cast<uint32_t*>(qm + mean_count(s));
+  uint32_t* lo = hi + rows * s.nkb;
   block_means_kernel<<<dim3((unsigned)(s.nqb + s.nkb), (unsigned)chunks, (unsigned)B), 256, 0, st>>>(
       static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k), qm, km, s, flag);
-  block_scores_kernel<<<dim3((unsigned)kt, (unsigned)qt, (unsigned)bh), 64, 0, st>>>(qm, km, keys, s, flag);
+  block_scores_kernel<<<dim3((unsigned)kt, (unsigned)qt, (unsigned)bh), 64, 0, st>>>(qm, km, hi, lo, s, flag);
   unsigned char* out = static_cast<unsigned char*>(blocks);
   const unsigned picks = (unsigned)((rows + 7) / 8);
-  if (s.nkb <= 128) block_pick_kernel<4><<<picks, 256, 0, st>>>(keys, out, rows, s, flag);
-  else if (s.nkb <= 256) block_pick_kernel<8><<<picks, 256, 0, st>>>(keys, out, rows, s, flag);
-  else if (s.nkb <= 640) block_pick_kernel<20><<<picks, 256, 0, st>>>(keys, out, rows, s, flag);
-  else block_pick_kernel<0><<<picks, 256, 0, st>>>(keys, out, rows, s, flag);
+  if (s.nkb <= 128) block_pick_kernel<4><<<picks, 256, 0, st>>>(hi, lo, out, rows, s, flag);
+  else if (s.nkb <= 256) block_pick_kernel<8><<<picks, 256, 0, st>>>(hi, lo, out, rows, s, flag);
+  else if (s.nkb <= 640) block_pick_kernel<20><<<picks, 256, 0, st>>>(hi, lo, out, rows, s, flag);
+  else block_pick_kernel<0><<<picks, 256, 0, st>>>(hi, lo, out, rows, s, flag);
   return cudaGetLastError() == cudaSuccess ? VDIT_OK : VDIT_ERR_CUDA;
 }
 

@@ -25,7 +25,8 @@
 
 namespace vdit {
 
-constexpr int kNormBwdThreads = 320;     // at most: warps * groups * 32 (256 with V = 4)
+constexpr int kNormBwdThreads = 256;     // at most: warps * groups * 32
+constexpr int kNormBwdSumRow = 8;        // a token's warps at most: 8,192 / 8 / 32 / V with V = 4
 constexpr int kNormBwdVecs = 4;          // V at most: heads * head_dim <= 8,192
 constexpr int kNormBwdMaxStages = 8;
 constexpr int kNormBwdMaxCtas = 320;     // CTAs per tensor (rows of the workspace)
@@ -43,11 +44,14 @@ struct NormBwdParams {
 };
 
 // kWide: the group is the token's whole heads*D vector; else a group is 1 .. 32
-// neighbouring lanes of one vector each.
-template <bool kWide, int V>
-__global__ void __launch_bounds__(V == 4 ? 256 : kNormBwdThreads, V == 1 ? 3 : 2)
+// neighbouring lanes of one vector each.  kThreads: the CTA's threads at most,
+// which sets the registers a thread may have (kThreads * registers: half of an
+// SM's, except for the widest tokens).
+template <bool kWide, int V, int kThreads>
+__global__ void __launch_bounds__(kThreads, V == 4 && kThreads > 160 ? 1 : 2)
     bwd_qk_norm_rope3d_kernel(const NormBwdParams p, RopeShape s) {
-  __shared__ float2 wsum[2][kNormBwdThreads / 32];      // [chunk parity][warp]: sums of x^2 and of x u w
+  // [chunk parity][token of the chunk][x^2, x u w][warp]: the warps' sums, zeros past them
+  __shared__ __align__(16) float wsum[2][kNormBwdThreads / 32][2][kNormBwdSumRow];
   __shared__ double inv_freq[kRopeMaxPairs];
   __shared__ __align__(8) uint64_t full[kNormBwdMaxStages];
   if (__syncthreads_or(watchdog_tripped())) return;     // all threads of the CTA decide alike
@@ -87,9 +91,8 @@ __global__ void __launch_bounds__(V == 4 ? 256 : kNormBwdThreads, V == 1 ? 3 : 2
 
   const uint32_t row_bytes = (uint32_t)nv * 16u;
   const long long n_chunks = (s.ntok + G - 1) / G;
-  const long long n_my = (n_chunks - 1 - blockIdx.x) / gridDim.x + 1;   // grid <= n_chunks
-  auto issue = [&](long long k) {                       // thread 0: chunk k of this CTA into its stage
-    const int st = (int)(k % p.stages);
+  const long long n_my = (n_chunks - 1 - blockIdx.x) / gridDim.x + 1;   // grid <= n_chunks; below 2^31 (host)
+  auto issue = [&](long long k, int st) {               // thread 0: chunk k of this CTA into stage st = k mod stages
     const long long tok = (blockIdx.x + k * gridDim.x) * G;
     const uint32_t bytes = (uint32_t)min((long long)G, s.ntok - tok) * row_bytes;
     uint4* to = ring + (size_t)st * 2 * G * nv;
@@ -99,7 +102,7 @@ __global__ void __launch_bounds__(V == 4 ? 256 : kNormBwdThreads, V == 1 ? 3 : 2
   };
   long long issued = n_my < p.stages ? n_my : p.stages;
   if (t == 0)
-    for (long long k = 0; k < issued; ++k) issue(k);
+    for (int k = 0; k < (int)issued; ++k) issue(k, k);
   // the tables are built while the first rows land: rope_phasor's arithmetic
   for (int x = t; x < n_tab; x += T) {
     int pos, pi;
@@ -111,139 +114,171 @@ __global__ void __launch_bounds__(V == 4 ? 256 : kNormBwdThreads, V == 1 ? 3 : 2
     tab[x] = make_float2((float)cn, (float)sn);
   }
   __syncthreads();
-  // the pairs of chunk k's tokens, from the axis tables
-  auto pairs = [&](long long k) {
-    const long long tok0 = (blockIdx.x + k * gridDim.x) * G;
-    float2* to = reinterpret_cast<float2*>(cs + (k & 1) * 2 * G * vph);
+  // the pairs of a chunk's tokens, from the axis tables: thread x < G * P takes
+  // pair x % P of token x / P (P <= 128 and G <= 8 fit in the CTA four times), at
+  // positions that are stepped from chunk to chunk without a 64-bit division
+  const unsigned L = (unsigned)s.L, hw = (unsigned)(s.Hg * s.Wg), Wg = (unsigned)s.Wg;
+  unsigned l0 = (unsigned)((unsigned long long)blockIdx.x * G % L);          // the chunk's first token in its clip
+  const unsigned l_step = (unsigned)((unsigned long long)gridDim.x * G % L);
+  auto pairs = [&](int parity) {
+    float2* to = reinterpret_cast<float2*>(cs + parity * 2 * G * vph);
     for (int x = t; x < G * P; x += T) {
       const int j = x / P, pi = x - j * P;
-      if (tok0 + j >= s.ntok) break;
-      const int l = (int)((tok0 + j) % s.L);
-      float2 c;
-      if (pi < pt) c = tab[(l / (s.Hg * s.Wg)) * pt + pi];
-      else if (pi < pt + ph) c = tab[off_h + ((l / s.Wg) % s.Hg) * ph + (pi - pt)];
-      else c = tab[off_w + (l % s.Wg) * pw + (pi - pt - ph)];
-      to[((j * 2 + ((pi >> 1) & 1)) * vph + (pi >> 2)) * 2 + (pi & 1)] = c;
+      const unsigned l = (l0 + j) % L;                   // rows past the last token are filled too, and not read
+      int at;
+      if (pi < pt) {
+        at = (int)(l / hw) * pt + pi;
+      } else {
+        const unsigned r = l % hw, y = r / Wg;
+        at = pi < pt + ph ? off_h + (int)y * ph + (pi - pt) : off_w + (int)(r - y * Wg) * pw + (pi - pt - ph);
+      }
+      to[((j * 2 + ((pi >> 1) & 1)) * vph + (pi >> 2)) * 2 + (pi & 1)] = tab[at];
     }
+    l0 += l_step;
+    if (l0 >= L) l0 -= L;
   };
   pairs(0);
 
+  for (int x = t; x < (int)(sizeof(wsum) / 4); x += T) (&wsum[0][0][0][0])[x] = 0.f;
+
   constexpr int NW = kWide ? V : 1;                     // vectors of a thread with channels of their own
-  constexpr bool kHoldW = NW <= 2;                      // their weights fit the registers too
   const int gv = p.group / 8;                           // vectors per group
   const float inv_group = 1.f / (float)p.group;
-  float2 dw[NW][4], wv[NW][4];
-  auto load_w = [&](int e, float2 (&to)[4]) {           // the vector's weights
-    if (w != nullptr) {
-      const float* at = w + (e * 8) % p.group;
-      const float4 a = __ldg(reinterpret_cast<const float4*>(at));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(at + 4));
-      to[0] = make_float2(a.x, a.y); to[1] = make_float2(a.z, a.w);
-      to[2] = make_float2(b.x, b.y); to[3] = make_float2(b.z, b.w);
-    } else {
-#pragma unroll
-      for (int m = 0; m < 4; ++m) to[m] = make_float2(1.f, 1.f);
-    }
-  };
+  float dw[NW][8], wv[NW][8];
 #pragma unroll
   for (int r = 0; r < NW; ++r) {
+    const int e = li + span * r;
+    const bool have = w != nullptr && e < nv;
+    const float* at = w + (e * 8) % p.group;
+    const float4 a = have ? __ldg(reinterpret_cast<const float4*>(at)) : make_float4(1.f, 1.f, 1.f, 1.f);
+    const float4 b = have ? __ldg(reinterpret_cast<const float4*>(at + 4)) : a;
+    wv[r][0] = a.x; wv[r][1] = a.y; wv[r][2] = a.z; wv[r][3] = a.w;
+    wv[r][4] = b.x; wv[r][5] = b.y; wv[r][6] = b.z; wv[r][7] = b.w;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) dw[r][m] = make_float2(0.f, 0.f);
-    if (kHoldW && li + span * r < nv) load_w(li + span * r, wv[r]);
+    for (int m = 0; m < 8; ++m) dw[r][m] = 0.f;
   }
-  auto pair_of = [](uint32_t b) { return make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u)); };
-  __syncthreads();                                      // pairs(0)
+  auto lo = [](uint32_t b) { return __uint_as_float(b << 16); };
+  auto hi = [](uint32_t b) { return __uint_as_float(b & 0xffff0000u); };
+  // What a thread reads and writes steps from chunk to chunk by constants.  Only
+  // the last chunk can have fewer than G tokens, and only a CTA's last vectors can
+  // lie past the token.
+  bool in[V];
+  int cs_at[V];
+#pragma unroll
+  for (int r = 0; r < V; ++r) {
+    const int e = li + span * r;
+    in[r] = gi < G && e < nv;
+    cs_at[r] = gi * 2 * vph + e % vph;
+  }
+  const bool last_live = (blockIdx.x + (n_my - 1) * gridDim.x) * G + gi < s.ntok;
+  uint4* dst = reinterpret_cast<uint4*>(d_out) + ((long long)blockIdx.x * G + gi) * nv + li;
+  const long long dst_step = (long long)gridDim.x * G * nv;
+  const int sg_off = G * nv, stage_vecs = 2 * G * nv, cs_step = 2 * G * vph;
+  const uint4* sx = ring + gi * nv + li;
+  const int my = (int)n_my;
+  __syncthreads();                                      // pairs(0), the zeros
 
-  long long k = 0;
-  for (; k < n_my; ++k) {
-    const long long tok = (blockIdx.x + k * gridDim.x) * G + gi;
-    const int par = (int)(k & 1);
-    const int st = (int)(k % p.stages);
-    const bool live = gi < G && tok < s.ntok;
-    const bool okw = mbar_wait(&full[st], (uint32_t)((k / p.stages) & 1), kSiteNormBwdFull);
-    const uint4* sx = ring + ((size_t)st * 2 * G + gi) * nv;
-    const uint4* sg = sx + (size_t)G * nv;
-    const float4* c4 = cs + (par * G + gi) * 2 * vph;
+  int k = 0, st = 0, par = 0;                           // k mod stages, k mod 2
+  uint32_t phase = 0;
+  for (; k < my; ++k) {
+    const bool live = k + 1 < my || last_live;
+    const bool okw = mbar_wait(&full[st], phase, kSiteNormBwdFull);
+    const float4* c4 = cs + par * cs_step;
     uint4 x[V];
-    float2 u[V][4];
-    float2 sum[kWide ? 1 : V];                          // x^2 and x u w
+    float u[V][8];
+    float sq[kWide ? 1 : V], dot[kWide ? 1 : V];        // sums of x^2 and of x u w
 #pragma unroll
     for (int r = 0; r < V; ++r) {
-      const int e = li + span * r;
-      float2 a = make_float2(0.f, 0.f), d = a;
-      if (live && okw && e < nv) {
-        x[r] = sx[e];
-        const uint4 g = sg[e];
-        const int vi = e % vph;
-        const float4 ca = c4[vi], cb = c4[vph + vi];
+      float a = 0.f, d = 0.f;
+      if (in[r] && live && okw) {
+        x[r] = sx[st * stage_vecs + span * r];
+        const uint4 g = sx[st * stage_vecs + sg_off + span * r];
+        const float4 ca = c4[cs_at[r]], cb = c4[cs_at[r] + vph];
         // u = R^T g: (g0, g1) -> (g0 cos + g1 sin, g1 cos - g0 sin)
-        auto back = [&](uint32_t b, float c, float sn) {
-          const float2 y = pair_of(b);
-          return make_float2(fmaf(y.x, c, y.y * sn), fmaf(y.y, c, -(y.x * sn)));
+        auto back = [&](uint32_t b, float c, float sn, float& u0, float& u1) {
+          const float g0 = lo(b), g1 = hi(b);
+          u0 = fmaf(g0, c, g1 * sn);
+          u1 = fmaf(g1, c, -(g0 * sn));
         };
-        u[r][0] = back(g.x, ca.x, ca.y);
-        u[r][1] = back(g.y, ca.z, ca.w);
-        u[r][2] = back(g.z, cb.x, cb.y);
-        u[r][3] = back(g.w, cb.z, cb.w);
-        float2 we[4];
-        if (!kHoldW) load_w(e, we);
+        back(g.x, ca.x, ca.y, u[r][0], u[r][1]);
+        back(g.y, ca.z, ca.w, u[r][2], u[r][3]);
+        back(g.z, cb.x, cb.y, u[r][4], u[r][5]);
+        back(g.w, cb.z, cb.w, u[r][6], u[r][7]);
         const uint32_t xs[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const float2 y = pair_of(xs[m]);
-          a = ffma2(y, y, a);
-          d = ffma2(y, fmul2(u[r][m], kHoldW ? wv[kWide ? r : 0][m] : we[m]), d);
+          const float x0 = lo(xs[m]), x1 = hi(xs[m]);
+          const float* wr = wv[kWide ? r : 0];
+          a = fmaf(x0, x0, a);
+          d = fmaf(x0, u[r][2 * m] * wr[2 * m], d);
+          a = fmaf(x1, x1, a);
+          d = fmaf(x1, u[r][2 * m + 1] * wr[2 * m + 1], d);
         }
       }
-      const float2 one = make_float2(a.x + a.y, d.x + d.y);
-      if (kWide && r > 0) sum[0] = fadd2(sum[0], one);
-      else sum[kWide ? 0 : r] = one;
+      if (kWide && r > 0) {
+        sq[0] += a;
+        dot[0] += d;
+      } else {
+        sq[kWide ? 0 : r] = a;
+        dot[kWide ? 0 : r] = d;
+      }
     }
-    auto add_lanes = [&](float2& v, int o) {
-      v = fadd2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
-    };
     if (kWide) {
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) add_lanes(sum[0], o);
-      if (lane == 0) wsum[par][warp] = sum[0];
+      for (int o = 16; o >= 1; o >>= 1) {
+        sq[0] += __shfl_xor_sync(0xffffffffu, sq[0], o);
+        dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], o);
+      }
+      if (lane == 0) {
+        wsum[par][gi][0][warp - gi * p.warps] = sq[0];
+        wsum[par][gi][1][warp - gi * p.warps] = dot[0];
+      }
     } else {
+      for (int o = gv >> 1; o >= 1; o >>= 1) {
 #pragma unroll
-      for (int r = 0; r < V; ++r)
-        for (int o = gv >> 1; o >= 1; o >>= 1) add_lanes(sum[kWide ? 0 : r], o);
+        for (int r = 0; r < V; ++r) {
+          sq[kWide ? 0 : r] += __shfl_xor_sync(0xffffffffu, sq[kWide ? 0 : r], o);
+          dot[kWide ? 0 : r] += __shfl_xor_sync(0xffffffffu, dot[kWide ? 0 : r], o);
+        }
+      }
     }
-    if (k + 1 < n_my) pairs(k + 1);
+    if (k + 1 < my) pairs(par ^ 1);
     if (!__syncthreads_and(okw)) break;                 // the stage is free; the sums and the next pairs are out
-    if (t == 0 && issued < n_my) issue(issued++);
+    if (t == 0 && issued < my) issue(issued++, st);
     if (kWide) {
-      sum[0] = wsum[par][gi * p.warps];
-      for (int i = 1; i < p.warps; ++i) sum[0] = fadd2(sum[0], wsum[par][gi * p.warps + i]);
+      float* both[2] = {&sq[0], &dot[0]};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4* at = reinterpret_cast<const float4*>(wsum[par][gi][i]);
+        const float4 a = at[0], b = at[1];
+        *both[i] = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+      }
     }
-    uint4* dst = reinterpret_cast<uint4*>(d_out) + tok * nv;
 #pragma unroll
     for (int r = 0; r < V; ++r) {
-      const int e = li + span * r;
-      if (live && e < nv) {
-        const float2 sm = sum[kWide ? 0 : r];
-        const float rr = rsqrtf(fmaf(sm.x, inv_group, p.eps));
-        const float back = -(rr * rr) * (sm.y * inv_group);   // dx = rr (u w + x back)
-        const float2 rr2 = make_float2(rr, rr), bk2 = make_float2(back, back);
-        float2 we[4];
-        if (!kHoldW) load_w(e, we);
+      if (in[r] && live) {
+        const float rr = rsqrtf(fmaf(sq[kWide ? 0 : r], inv_group, p.eps));
+        const float back = -(rr * rr) * (dot[kWide ? 0 : r] * inv_group);   // dx = rr (u w + x back)
         const uint32_t xs[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+        const float* wr = wv[kWide ? r : 0];
+        float* dwr = dw[kWide ? r : 0];
         uint32_t o[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const int rw = kWide ? r : 0;
-          const float2 y = pair_of(xs[m]);
-          const float2 dx = fmul2(rr2, ffma2(y, bk2, fmul2(u[r][m], kHoldW ? wv[rw][m] : we[m])));
-          dw[rw][m] = ffma2(u[r][m], fmul2(y, rr2), dw[rw][m]);
-          o[m] = pack_bf16x2(dx.x, dx.y);
+          const float x0 = lo(xs[m]), x1 = hi(xs[m]);
+          const float u0 = u[r][2 * m], u1 = u[r][2 * m + 1];
+          o[m] = pack_bf16x2(rr * fmaf(x0, back, u0 * wr[2 * m]), rr * fmaf(x1, back, u1 * wr[2 * m + 1]));
+          dwr[2 * m] = fmaf(u0, x0 * rr, dwr[2 * m]);
+          dwr[2 * m + 1] = fmaf(u1, x1 * rr, dwr[2 * m + 1]);
         }
-        dst[e] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[span * r] = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
+    dst += dst_step;
+    par ^= 1;
+    if (++st == p.stages) { st = 0; phase ^= 1u; }
   }
-  const bool whole = k == n_my;
+  const bool whole = k == my;
   // No copy may still be landing in shared memory when the CTA exits (only
   // when a wait above ran out can chunks k .. issued-1 still be in flight).
   if (t == 0)
@@ -251,55 +286,53 @@ __global__ void __launch_bounds__(V == 4 ? 256 : kNormBwdThreads, V == 1 ? 3 : 2
       mbar_drain_site(&full[k2 % p.stages], (uint32_t)((k2 / p.stages) & 1), kSiteNormBwdDrain);
   if (p.parts == nullptr || !whole) return;
   float* out = p.parts + ((long long)tensor * kNormBwdMaxCtas + blockIdx.x) * p.group;
-  if (kWide && V > 1) {                                 // one token per chunk: a channel is one thread's
-#pragma unroll
-    for (int r = 0; r < V; ++r) {
-      const int e = li + span * r;
-      if (e < nv) {
-        float4* to = reinterpret_cast<float4*>(out + e * 8);
-        to[0] = make_float4(dw[kWide ? r : 0][0].x, dw[kWide ? r : 0][0].y, dw[kWide ? r : 0][1].x, dw[kWide ? r : 0][1].y);
-        to[1] = make_float4(dw[kWide ? r : 0][2].x, dw[kWide ? r : 0][2].y, dw[kWide ? r : 0][3].x, dw[kWide ? r : 0][3].y);
-      }
-    }
-    return;
-  }
   // threads t, t + step, t + 2 step, ... hold the same channels
   const int step = kWide ? span : gv;
   float* all = reinterpret_cast<float*>(dyn_smem);      // [T][8], over the ring
-  float2* mine = reinterpret_cast<float2*>(all + t * 8);
 #pragma unroll
-  for (int m = 0; m < 4; ++m) mine[m] = dw[0][m];
-  __syncthreads();
-  for (int c = t; c < p.group; c += T) {
-    float a = 0.f;
-    for (int i = c >> 3; i < T; i += step) a += all[i * 8 + (c & 7)];
-    out[c] = a;
+  for (int r = 0; r < NW; ++r) {
+    if (r > 0) __syncthreads();
+#pragma unroll
+    for (int m = 0; m < 8; ++m) all[t * 8 + m] = dw[r][m];
+    __syncthreads();
+    for (int c = t; c < min(step * 8, p.group - r * span * 8); c += T) {
+      float a = 0.f;
+      for (int i = c >> 3; i < T; i += step) a += all[i * 8 + (c & 7)];
+      out[r * span * 8 + c] = a;
+    }
   }
 }
 
 // dw[c] = the CTAs' parts of channel c, added in a fixed order: a CTA takes 32
-// channels of one tensor, its eight warps the CTAs w, w + 8, ...
-__global__ void __launch_bounds__(256) bwd_weights_qk_norm_rope3d_kernel(const float* __restrict__ parts, float* dwq,
-                                                                         float* dwk, int group, int n_parts) {
-  __shared__ float sum[8][32];
+// channels of one tensor, its 32 warps the CTAs w, w + 32, ... (at most ten loads
+// each, all in flight at once).
+__global__ void __launch_bounds__(1024) bwd_weights_qk_norm_rope3d_kernel(const float* __restrict__ parts, float* dwq,
+                                                                          float* dwk, int group, int n_parts) {
+  __shared__ float sum[32][33];
   if (watchdog_tripped()) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* dw = blockIdx.y ? dwk : dwq;
+  if (dw == nullptr) return;
   const float* from = parts + (long long)blockIdx.y * kNormBwdMaxCtas * group;
   const int c = blockIdx.x * 32 + lane;
-  float a = 0.f;
-  if (dw != nullptr && c < group) {
-#pragma unroll 4
-    for (int i = warp; i < n_parts; i += 8) a += from[(long long)i * group + c];
+  constexpr int kEach = kNormBwdMaxCtas / 32;
+  float v[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int row = warp + 32 * i;
+    v[i] = c < group && row < n_parts ? __ldg(from + (long long)row * group + c) : 0.f;
   }
+  float a = v[0];
+#pragma unroll
+  for (int i = 1; i < kEach; ++i) a += v[i];
   sum[warp][lane] = a;
   __syncthreads();
-  if (warp == 0 && dw != nullptr && c < group) {
-    float b = 0.f;
+  // warp w adds channel w's 32 parts
+  float b = sum[lane][warp];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b += sum[i][lane];
-    dw[c] = b;
-  }
+  for (int o = 16; o >= 1; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
+  const int ch = blockIdx.x * 32 + warp;
+  if (lane == 0 && ch < group) dw[ch] = b;
 }
 
 }  // namespace vdit

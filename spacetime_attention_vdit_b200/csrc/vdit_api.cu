@@ -414,21 +414,56 @@ int launch_block_sparse_bwd(const void* q, const void* k, const void* v, const v
   return last_launch_status();
 }
 
-template <int V>
-int launch_norm_rope_bwd(bool wide, const NormBwdParams& p, const RopeShape& s, dim3 grid, int threads, int smem,
-                         int smem_limit, cudaStream_t stream) {
+// `tab`: entries of the per-axis tables.  *parts: CTAs per tensor.
+template <int V, int kThreads>
+int launch_norm_rope_bwd(bool wide, NormBwdParams p, const RopeShape& s, long long tab, int* parts,
+                         cudaStream_t stream) {
+  constexpr int kMost = 224 * 1024;                      // shared memory of an SM that the CTAs share
   static bool done_n[kMaxDevices] = {}, done_w[kMaxDevices] = {};
+  static int regs[2][kMaxDevices];
   static std::mutex mu;
+  auto kernel = wide ? bwd_qk_norm_rope3d_kernel<true, V, kThreads> : bwd_qk_norm_rope3d_kernel<false, V, kThreads>;
+  int dev = 0, my_regs;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return VDIT_ERR_CUDA;
   {
     std::lock_guard<std::mutex> lock(mu);
-    if (!ensure_smem(bwd_qk_norm_rope3d_kernel<false, V>, smem_limit, done_n) ||
-        !ensure_smem(bwd_qk_norm_rope3d_kernel<true, V>, smem_limit, done_w))
-      return VDIT_ERR_CUDA;
+    bool(&done)[kMaxDevices] = wide ? done_w : done_n;
+    if (!done[dev]) {
+      cudaFuncAttributes a;
+      if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess) return VDIT_ERR_CUDA;
+      regs[wide][dev] = a.numRegs;
+    }
+    if (!ensure_smem(kernel, kMost, done)) return VDIT_ERR_CUDA;
+    my_regs = regs[wide][dev];
   }
-  if (wide)
-    bwd_qk_norm_rope3d_kernel<true, V><<<grid, threads, smem, stream>>>(p, s);
-  else
-    bwd_qk_norm_rope3d_kernel<false, V><<<grid, threads, smem, stream>>>(p, s);
+  // Up to four CTAs share an SM, as the registers allow; three or fewer where
+  // that leaves less than two stages each.  Shared memory of one: the ring (x and g rows of
+  // `stages` chunks), two chunks' pairs and the per-axis tables.
+  const int threads = 32 * p.warps * p.groups;
+  const long long stage = 4LL * s.heads * s.D * p.groups;
+  const long long fixed = 2LL * p.groups * s.D / 2 * 8 + tab * 8;
+  int per_sm = 65536 / (threads * ((my_regs + 7) / 8 * 8));
+  if (per_sm > 4) per_sm = 4;
+  if (per_sm < 1) per_sm = 1;
+  long long stages = (kMost / per_sm - 4096 - fixed) / stage;
+  while (stages < 2 && per_sm > 1) {
+    --per_sm;
+    stages = (kMost / per_sm - 4096 - fixed) / stage;
+  }
+  if (stages > kNormBwdMaxStages) stages = kNormBwdMaxStages;
+  p.stages = (int)stages;                                // at least 4: 154 KB over a 32 KB stage
+  long long smem = stages * stage + fixed;
+  if (smem < threads * 32) smem = threads * 32;          // the threads' parts of the weight gradient meet there
+  const long long chunks = (s.ntok + p.groups - 1) / p.groups;
+  // half of the CTAs for each tensor; K alone takes no more, so that its weight
+  // gradient is summed in the same order as beside Q
+  long long ctas = (long long)sm_count() * per_sm / 2;
+  if (ctas > kNormBwdMaxCtas) ctas = kNormBwdMaxCtas;
+  if (ctas > chunks) ctas = chunks;
+  if (ctas < 1) ctas = 1;
+  if (chunks / ctas >= 0x7fffffffLL) return VDIT_ERR_SHAPE;
+  *parts = (int)ctas;
+  kernel<<<dim3((unsigned)ctas, (unsigned)s.ntens), threads, (size_t)smem, stream>>>(p, s);
   return last_launch_status();
 }
 
@@ -884,44 +919,26 @@ int vdit_qk_norm_rope_3d_bwd(const void* q, const void* k, const void* gq, const
   p.group = norm_group;
   p.eps = eps;
   p.theta = (double)theta;
-  // V vectors per thread, `warps` warps per token, `groups` tokens per CTA: as
-  // few vectors per thread as 320 threads cover, then as many tokens as 8 warps
+  // V vectors per thread, `warps` warps per token: the V with the fewest idle
+  // slots, of equal ones the largest (what a warp does once per token - its
+  // sums' shuffles, the barrier, the loop - weighs as much as two vectors); then
+  // tokens up to four warps a CTA.
   const int nv = (int)(width / 8);
-  const int V = (nv + kNormBwdThreads - 1) / kNormBwdThreads;
+  int V = 1;
+  for (int v = 2; v <= kNormBwdVecs; ++v)
+    if ((nv + 32 * v - 1) / (32 * v) * v <= (nv + 32 * V - 1) / (32 * V) * V || nv > 32 * V * (kNormBwdThreads / 32)) V = v;
   p.warps = (nv + 32 * V - 1) / (32 * V);
-  p.groups = p.warps >= 8 ? 1 : 8 / p.warps;
-  const int threads = 32 * p.warps * p.groups;
-  // Shared memory: the ring (x and g rows of `stages` chunks), two chunks' pairs
-  // and the per-axis tables.  Three CTAs (V = 1) or two share an SM where two
-  // stages each fit, else one takes it.
-  constexpr long long kMost = 224 * 1024;
-  const long long stage = 4 * width * p.groups;
-  const long long fixed = 2LL * p.groups * head_dim / 2 * 8 + tab * 8;
-  int per_sm = V == 1 ? 3 : 2;
-  long long stages = (kMost / per_sm - 2048 - fixed) / stage;
-  while (stages < 2 && per_sm > 1) {
-    --per_sm;
-    stages = (kMost / per_sm - 2048 - fixed) / stage;
-  }
-  if (stages > kNormBwdMaxStages) stages = kNormBwdMaxStages;
-  p.stages = (int)stages;                              // at least 4: 156 KB over a 32 KB stage
-  long long smem = stages * stage + fixed;
-  if (smem < threads * 32) smem = threads * 32;        // the threads' parts of the weight gradient meet there
-  const long long chunks = (s.ntok + p.groups - 1) / p.groups;
-  // half of the CTAs for each tensor; K alone takes no more, so that its weight
-  // gradient is summed in the same order as beside Q
-  long long ctas = (long long)sm_count() * per_sm / 2;
-  if (ctas > kNormBwdMaxCtas) ctas = kNormBwdMaxCtas;
-  if (ctas > chunks) ctas = chunks;
-  const dim3 grid((unsigned)ctas, (unsigned)s.ntens);
+  p.groups = p.warps >= 4 ? 1 : 4 / p.warps;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  rc = V == 1   ? launch_norm_rope_bwd<1>(wide, p, s, grid, threads, (int)smem, (int)kMost, st)
-       : V == 2 ? launch_norm_rope_bwd<2>(wide, p, s, grid, threads, (int)smem, (int)kMost, st)
-       : V == 3 ? launch_norm_rope_bwd<3>(wide, p, s, grid, threads, (int)smem, (int)kMost, st)
-                : launch_norm_rope_bwd<4>(wide, p, s, grid, threads, (int)smem, (int)kMost, st);
+  int parts = 0;
+  rc = V == 1          ? launch_norm_rope_bwd<1, 256>(wide, p, s, tab, &parts, st)
+       : V == 2        ? launch_norm_rope_bwd<2, 256>(wide, p, s, tab, &parts, st)
+       : V == 3        ? launch_norm_rope_bwd<3, 256>(wide, p, s, tab, &parts, st)
+       : p.warps <= 5 ? launch_norm_rope_bwd<4, 160>(wide, p, s, tab, &parts, st)
+                       : launch_norm_rope_bwd<4, 256>(wide, p, s, tab, &parts, st);
   if (rc != VDIT_OK || !weights) return rc;
-  bwd_weights_qk_norm_rope3d_kernel<<<dim3((unsigned)((norm_group + 31) / 32), 2), 256, 0, st>>>(
-      p.parts, k_only ? nullptr : dwq, dwk, norm_group, (int)ctas);
+  bwd_weights_qk_norm_rope3d_kernel<<<dim3((unsigned)((norm_group + 31) / 32), 2), 1024, 0, st>>>(
+      p.parts, k_only ? nullptr : dwq, dwk, norm_group, parts);
   return last_launch_status();
 }
 

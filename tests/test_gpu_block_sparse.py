@@ -101,7 +101,7 @@ def _check_backward(q, k, v, blocks, scale=0.0, seed=9):
 @pytest.mark.parametrize("B,Lq,Lk,heads,D,top_k", [
     (1, 1, 1, 1, 32, 1), (1, 128, 128, 2, 64, 1), (2, 129, 640, 3, 32, 2), (1, 1000, 1000, 5, 128, 8),
     (1, 1, 4100, 2, 128, 33), (2, 777, 5000, 2, 64, 39), (1, 9000, 300, 1, 128, 3), (1, 300, 9000, 3, 32, 1),
-    (1, 200, 9000, 1, 32, 71),
+    (1, 200, 9000, 1, 32, 71), (1, 300, 30000, 2, 32, 17), (1, 300, 82000, 1, 32, 100), (1, 140, 90000, 2, 32, 9),
 ])
 def test_select_matches_oracle(B, Lq, Lk, heads, D, top_k):
     import spacetime_attention_vdit_b200 as vd
@@ -140,6 +140,21 @@ def test_select_nan_infinite_and_denormal_scores():
         got = vd.attn_select_blocks(to_dev_bf16(q), to_dev_bf16(k), top_k).cpu().numpy()
         with np.errstate(all="ignore"):
             assert np.array_equal(got, sp.select_blocks(f64(q), f64(k), top_k)), top_k
+
+
+@pytest.mark.parametrize("n", [40, 200, 300, 700])
+def test_select_long_rows_decided_by_the_last_bits(n):
+    """Means that agree in their leading 40 bits, and some that are equal: the
+    threshold search has to go to the end, at every length of row."""
+    import spacetime_attention_vdit_b200 as vd
+    k = np.zeros((1, 128 * n, 1, 32), dtype=np.float32)
+    k[:, 0::128, 0, 0] = 1024.0
+    k[:, 1::128, 0, 0] = np.random.default_rng(n).integers(0, n // 3, n).astype(np.float32) * 2.0 ** -30
+    kb = synthetic.f32_to_bf16_bits(k)
+    q = np.full((1, 128, 1, 32), 0x3f80, dtype=np.uint16)
+    for top_k in (1, 2, n // 4, n // 2, n - 1, n):
+        got = vd.attn_select_blocks(to_dev_bf16(q), to_dev_bf16(kb), top_k).cpu().numpy()
+        assert np.array_equal(got, sp.select_blocks(f64(q), f64(kb), top_k)), top_k
 
 
 def test_select_values_next_to_a_border():
