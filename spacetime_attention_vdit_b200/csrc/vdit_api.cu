@@ -415,53 +415,41 @@ int launch_block_sparse_bwd(const void* q, const void* k, const void* v, const v
 }
 
 // `tab`: entries of the per-axis tables.  *parts: CTAs per tensor.
-template <int V, int kThreads>
+template <int V>
 int launch_norm_rope_bwd(bool wide, NormBwdParams p, const RopeShape& s, long long tab, int* parts,
                          cudaStream_t stream) {
-  constexpr int kMost = 224 * 1024;                      // shared memory of an SM that the CTAs share
+  constexpr int kMost = 220 * 1024;                      // dynamic shared memory, beside some 6 KB of static
   static bool done_n[kMaxDevices] = {}, done_w[kMaxDevices] = {};
-  static int regs[2][kMaxDevices];
   static std::mutex mu;
-  auto kernel = wide ? bwd_qk_norm_rope3d_kernel<true, V, kThreads> : bwd_qk_norm_rope3d_kernel<false, V, kThreads>;
-  int dev = 0, my_regs;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return VDIT_ERR_CUDA;
+  auto kernel = wide ? bwd_qk_norm_rope3d_kernel<true, V> : bwd_qk_norm_rope3d_kernel<false, V>;
   {
     std::lock_guard<std::mutex> lock(mu);
-    bool(&done)[kMaxDevices] = wide ? done_w : done_n;
-    if (!done[dev]) {
-      cudaFuncAttributes a;
-      if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess) return VDIT_ERR_CUDA;
-      regs[wide][dev] = a.numRegs;
-    }
-    if (!ensure_smem(kernel, kMost, done)) return VDIT_ERR_CUDA;
-    my_regs = regs[wide][dev];
+    if (!ensure_smem(kernel, kMost, wide ? done_w : done_n)) return VDIT_ERR_CUDA;
   }
-  // Up to four CTAs share an SM, as the registers allow; three or fewer where
-  // that leaves less than two stages each.  Shared memory of one: the ring (x and g rows of
-  // `stages` chunks), two chunks' pairs and the per-axis tables.
-  const int threads = 32 * p.warps * p.groups;
-  const long long stage = 4LL * s.heads * s.D * p.groups;
-  const long long fixed = 2LL * p.groups * s.D / 2 * 8 + tab * 8;
-  int per_sm = 65536 / (threads * ((my_regs + 7) / 8 * 8));
-  if (per_sm > 4) per_sm = 4;
-  if (per_sm < 1) per_sm = 1;
-  long long stages = (kMost / per_sm - 4096 - fixed) / stage;
-  while (stages < 2 && per_sm > 1) {
-    --per_sm;
-    stages = (kMost / per_sm - 4096 - fixed) / stage;
-  }
+  // One CTA per SM, of as many groups as its threads allow (no more than there
+  // are tokens for; a group of more than one warp takes one of 15 hardware
+  // barriers), each with two stages or more.  Shared memory: the rings (a stage: x
+  // and g rows of a token), two tokens' pairs per group, the weights, the tables.
+  const long long width = (long long)s.heads * s.D, stage = 4 * width;
+  const long long shared = (wide ? 4 * width : 0) + tab * 8, pair_rows = 2LL * s.D / 2 * 8;
+  const long long per_tensor = sm_count() / s.ntens < kNormBwdMaxCtas ? sm_count() / s.ntens : kNormBwdMaxCtas;
+  int G = norm_bwd_threads(V) / (32 * p.warps);
+  if (p.warps > 1 && G > 15) G = 15;
+  if (G > kNormBwdGroups) G = kNormBwdGroups;
+  const long long enough = (s.ntok + per_tensor - 1) / per_tensor;
+  if (G > enough) G = (int)enough;
+  auto stages_of = [&](int g) { return ((kMost - shared) / g - pair_rows) / stage; };
+  while (G > 1 && stages_of(G) < 2) --G;
+  long long stages = stages_of(G);                       // at least 3: 124 KB over a 32 KB stage
   if (stages > kNormBwdMaxStages) stages = kNormBwdMaxStages;
-  p.stages = (int)stages;                                // at least 4: 154 KB over a 32 KB stage
-  long long smem = stages * stage + fixed;
+  p.groups = G;
+  p.stages = (int)stages;
+  const int threads = 32 * p.warps * G;
+  long long smem = G * (stages * stage + pair_rows) + shared;
   if (smem < threads * 32) smem = threads * 32;          // the threads' parts of the weight gradient meet there
-  const long long chunks = (s.ntok + p.groups - 1) / p.groups;
-  // half of the CTAs for each tensor; K alone takes no more, so that its weight
-  // gradient is summed in the same order as beside Q
-  long long ctas = (long long)sm_count() * per_sm / 2;
-  if (ctas > kNormBwdMaxCtas) ctas = kNormBwdMaxCtas;
-  if (ctas > chunks) ctas = chunks;
-  if (ctas < 1) ctas = 1;
-  if (chunks / ctas >= 0x7fffffffLL) return VDIT_ERR_SHAPE;
+  long long ctas = (s.ntok + G - 1) / G;
+  if (ctas > per_tensor) ctas = per_tensor;
+  if (s.ntok / (ctas * G) >= 0x7ffffff0LL) return VDIT_ERR_SHAPE;
   *parts = (int)ctas;
   kernel<<<dim3((unsigned)ctas, (unsigned)s.ntens), threads, (size_t)smem, stream>>>(p, s);
   return last_launch_status();
@@ -921,21 +909,18 @@ int vdit_qk_norm_rope_3d_bwd(const void* q, const void* k, const void* gq, const
   p.theta = (double)theta;
   // V vectors per thread, `warps` warps per token: the V with the fewest idle
   // slots, of equal ones the largest (what a warp does once per token - its
-  // sums' shuffles, the barrier, the loop - weighs as much as two vectors); then
-  // tokens up to four warps a CTA.
+  // sums' shuffles, the barrier, the loop - weighs as much as two vectors).
   const int nv = (int)(width / 8);
   int V = 1;
   for (int v = 2; v <= kNormBwdVecs; ++v)
-    if ((nv + 32 * v - 1) / (32 * v) * v <= (nv + 32 * V - 1) / (32 * V) * V || nv > 32 * V * (kNormBwdThreads / 32)) V = v;
+    if ((nv + 32 * v - 1) / (32 * v) * v <= (nv + 32 * V - 1) / (32 * V) * V || nv > 32 * V * kNormBwdWarps) V = v;
   p.warps = (nv + 32 * V - 1) / (32 * V);
-  p.groups = p.warps >= 4 ? 1 : 4 / p.warps;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int parts = 0;
-  rc = V == 1          ? launch_norm_rope_bwd<1, 256>(wide, p, s, tab, &parts, st)
-       : V == 2        ? launch_norm_rope_bwd<2, 256>(wide, p, s, tab, &parts, st)
-       : V == 3        ? launch_norm_rope_bwd<3, 256>(wide, p, s, tab, &parts, st)
-       : p.warps <= 5 ? launch_norm_rope_bwd<4, 160>(wide, p, s, tab, &parts, st)
-                       : launch_norm_rope_bwd<4, 256>(wide, p, s, tab, &parts, st);
+  rc = V == 1   ? launch_norm_rope_bwd<1>(wide, p, s, tab, &parts, st)
+       : V == 2 ? launch_norm_rope_bwd<2>(wide, p, s, tab, &parts, st)
+       : V == 3 ? launch_norm_rope_bwd<3>(wide, p, s, tab, &parts, st)
+                : launch_norm_rope_bwd<4>(wide, p, s, tab, &parts, st);
   if (rc != VDIT_OK || !weights) return rc;
   bwd_weights_qk_norm_rope3d_kernel<<<dim3((unsigned)((norm_group + 31) / 32), 2), 1024, 0, st>>>(
       p.parts, k_only ? nullptr : dwq, dwk, norm_group, parts);

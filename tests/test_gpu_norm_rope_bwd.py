@@ -104,7 +104,8 @@ def _check_norm(B, grid, heads, D, split, group, eps=1e-6, weighted=True, seed=5
     only_k = vd.qk_norm_rope_3d_bwd(None, dev[1], None, dev[3], grid, group, None, wd[1], eps=eps, split=split)
     assert only_k[0] is None and only_k[2] is None and torch.equal(only_k[1], dk)
     if weighted:
-        assert torch.equal(only_k[3], dwk)
+        # K alone is split over more CTAs, so its sums are taken in another order
+        assert np.all(np.abs(only_k[3].cpu().numpy().astype(np.float64) - edw) <= (n * 2.0 ** -24 + 2e-5) * mw)
         again = vd.qk_norm_rope_3d_bwd(*dev, grid, group, *wd, eps=eps, split=split)
         assert all(torch.equal(a, b) for a, b in zip(again, (dq, dk, dwq, dwk)))
 
