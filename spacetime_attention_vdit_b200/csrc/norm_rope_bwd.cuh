@@ -52,6 +52,15 @@ struct NormBwdParams {
   double theta;
 };
 
+// What a group steps from token to token; in shared memory, since only a few of its
+// threads use it and all of them would hold it in registers.
+struct NormBwdGroup {
+  const __nv_bfloat16 *x, *g;   // the rows to be copied next
+  long long row_step;           // elements between the rows of two of its tokens
+  int pos[2][3];                // grid position (t, h, w) of the next token, by parity
+  int pos_step[3];
+};
+
 // kWide: the group is the token's whole heads*D vector; else a group is 1 .. 32
 // neighbouring lanes of one vector each.
 template <bool kWide, int V>
@@ -60,13 +69,11 @@ __global__ void __launch_bounds__(norm_bwd_threads(V), 1)
   // [group][token parity][x^2, x u w][warp]: the warps' sums, zeros past them
   __shared__ __align__(16) float wsum[kNormBwdGroups][2][2][kNormBwdWarps];
   __shared__ double inv_freq[kRopeMaxPairs];
+  __shared__ NormBwdGroup state[kNormBwdGroups];
   __shared__ __align__(8) uint64_t bars[kNormBwdGroups][kNormBwdMaxStages];
   if (__syncthreads_or(watchdog_tripped())) return;     // all threads of the CTA decide alike
 
   const int tensor = s.ntens == 2 ? (int)blockIdx.y : 1;
-  const __nv_bfloat16* x_in = tensor ? p.k : p.q;
-  const __nv_bfloat16* g_in = tensor ? p.gk : p.gq;
-  __nv_bfloat16* d_out = tensor ? p.dk : p.dq;
   const float* w = tensor ? p.wk : p.wq;
 
   const int T = blockDim.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -87,9 +94,19 @@ __global__ void __launch_bounds__(norm_bwd_threads(V), 1)
   const int pt = s.d_t / 2, ph = s.d_h / 2, pw = s.d_w / 2;
   const int Tg = (int)(s.L / ((long long)s.Hg * s.Wg));
   const int off_h = Tg * pt, off_w = off_h + s.Hg * ph, n_tab = off_w + s.Wg * pw;
+  NormBwdGroup& mine = state[gi];
+  // the group's tokens: first, first + step, ... (none, if there are more groups than tokens)
+  const long long first = (long long)blockIdx.x * G + gi, step = (long long)gridDim.x * G;
+  const int my = first < s.ntok ? (int)((s.ntok - 1 - first) / step + 1) : 0;   // below 2^31 (host)
   if (li == 0) {
     for (int st = 0; st < p.stages; ++st) mbar_init(&full[st], 1);
     fence_mbar_init();
+    mine.x = (tensor ? p.k : p.q) + first * nv * 8;
+    mine.g = (tensor ? p.gk : p.gq) + first * nv * 8;
+    mine.row_step = step * nv * 8;
+    const int hw = s.Hg * s.Wg, l = (int)(first % s.L), ls = (int)(step % s.L);
+    mine.pos[0][0] = l / hw; mine.pos[0][1] = l % hw / s.Wg; mine.pos[0][2] = l % s.Wg;
+    mine.pos_step[0] = ls / hw; mine.pos_step[1] = ls % hw / s.Wg; mine.pos_step[2] = ls % s.Wg;
   }
   for (int x = t; x < P; x += T) {
     int i, d;
@@ -104,20 +121,18 @@ __global__ void __launch_bounds__(norm_bwd_threads(V), 1)
       wsm[x] = w != nullptr ? __ldg(reinterpret_cast<const float4*>(w) + x) : make_float4(1.f, 1.f, 1.f, 1.f);
   __syncthreads();
 
-  // the group's tokens: first, first + step, ... (none, if there are more groups than tokens)
-  const uint32_t row_bytes = (uint32_t)nv * 16u;
-  const long long first = (long long)blockIdx.x * G + gi, step = (long long)gridDim.x * G;
-  const int my = first < s.ntok ? (int)((s.ntok - 1 - first) / step + 1) : 0;   // below 2^31 (host)
-  auto issue = [&](int k, int st) {                     // thread 0 of the group: its token k into stage k mod stages
-    const long long at = (first + k * step) * nv * 8;
+  auto issue = [&](int st) {                            // thread 0 of the group: its next token into a stage
+    const uint32_t row_bytes = (uint32_t)nv * 16u;
     uint4* to = ring + (size_t)st * 2 * nv;
     mbar_arrive_expect_tx(&full[st], 2 * row_bytes);
-    bulk_load(to, x_in + at, row_bytes, &full[st]);
-    bulk_load(to + nv, g_in + at, row_bytes, &full[st]);
+    bulk_load(to, mine.x, row_bytes, &full[st]);
+    bulk_load(to + nv, mine.g, row_bytes, &full[st]);
+    mine.x += mine.row_step;
+    mine.g += mine.row_step;
   };
   int issued = my < p.stages ? my : p.stages;
   if (li == 0)
-    for (int k = 0; k < issued; ++k) issue(k, k);
+    for (int k = 0; k < issued; ++k) issue(k);
   // the tables are built while the first rows land: rope_phasor's arithmetic
   for (int x = t; x < n_tab; x += T) {
     int pos, pi;
@@ -130,25 +145,24 @@ __global__ void __launch_bounds__(norm_bwd_threads(V), 1)
   }
   __syncthreads();
   // The pairs of the group's next token, from the tables; its grid position is
-  // stepped from token to token, so that nothing is divided.
-  const int hw = s.Hg * s.Wg;
-  const int l0 = (int)(first % s.L), ls = (int)(step % s.L);
-  int pos_t = l0 / hw, pos_h = l0 % hw / s.Wg, pos_w = l0 % s.Wg;
-  const int step_t = ls / hw, step_h = ls % hw / s.Wg, step_w = ls % s.Wg;
+  // stepped from token to token (thread 0 writes the one after next), so that
+  // nothing is divided.
   auto pairs = [&](int parity) {
     float2* to = reinterpret_cast<float2*>(cs + parity * 2 * vph);
     for (int pi = li; pi < P; pi += span) {
-      const int at = pi < pt        ? pos_t * pt + pi
-                     : pi < pt + ph ? off_h + pos_h * ph + (pi - pt)
-                                    : off_w + pos_w * pw + (pi - pt - ph);
+      const int at = pi < pt        ? mine.pos[parity][0] * pt + pi
+                     : pi < pt + ph ? off_h + mine.pos[parity][1] * ph + (pi - pt)
+                                    : off_w + mine.pos[parity][2] * pw + (pi - pt - ph);
       to[(((pi >> 1) & 1) * vph + (pi >> 2)) * 2 + (pi & 1)] = tab[at];
     }
-    pos_w += step_w;
-    if (pos_w >= s.Wg) { pos_w -= s.Wg; ++pos_h; }
-    pos_h += step_h;
-    if (pos_h >= s.Hg) { pos_h -= s.Hg; ++pos_t; }
-    pos_t += step_t;
-    if (pos_t >= Tg) pos_t -= Tg;
+    if (li == 0) {
+      int pos_t = mine.pos[parity][0] + mine.pos_step[0], pos_h = mine.pos[parity][1] + mine.pos_step[1],
+          pos_w = mine.pos[parity][2] + mine.pos_step[2];
+      if (pos_w >= s.Wg) { pos_w -= s.Wg; ++pos_h; }
+      if (pos_h >= s.Hg) { pos_h -= s.Hg; ++pos_t; }
+      if (pos_t >= Tg) pos_t -= Tg;
+      mine.pos[parity ^ 1][0] = pos_t; mine.pos[parity ^ 1][1] = pos_h; mine.pos[parity ^ 1][2] = pos_w;
+    }
   };
   pairs(0);
 
@@ -179,8 +193,8 @@ __global__ void __launch_bounds__(norm_bwd_threads(V), 1)
   // where a vector lies in its head: the same for all V where 32 * warps is a
   // whole number of heads, and then its pairs are read once
   const bool same = span % vph == 0;
-  uint4* dst = reinterpret_cast<uint4*>(d_out) + first * nv + li;
-  const long long dst_step = step * nv;
+  const int vi0 = li % vph;
+  uint4* dst = reinterpret_cast<uint4*>(tensor ? p.dk : p.dq) + first * nv + li;
   const int bar_id = 1 + (gi < 15 ? gi : 0);            // a hardware barrier per group; one-warp groups need none
   __syncthreads();                                      // pairs(0), the zeros
 
@@ -201,7 +215,7 @@ __global__ void __launch_bounds__(norm_bwd_threads(V), 1)
         x[r] = sx[span * r];
         const uint4 g = sx[nv + span * r];
         if (r == 0 || !same) {
-          const int vi = (li + span * r) % vph;
+          const int vi = r == 0 ? vi0 : (li + span * r) % vph;
           ca = c4[vi];
           cb = c4[vph + vi];
         }
@@ -263,19 +277,25 @@ __global__ void __launch_bounds__(norm_bwd_threads(V), 1)
       all = named_bar_and(bar_id, span, okw);
     }
     if (!all) break;
-    if (li == 0 && issued < my) { issue(issued, st); ++issued; }
+    if (li == 0 && issued < my) issue(st);
+    ++issued;
     if (kWide) {
       const float4* at = reinterpret_cast<const float4*>(wsum[gi][par][0]);
       const float4 a = at[0], b = at[1], c = at[2], d = at[3];
       sq[0] = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
       dot[0] = ((c.x + c.y) + (c.z + c.w)) + ((d.x + d.y) + (d.z + d.w));
     }
+    // dx = (u r) w - x r^3 mean(x u w); (u r) x is dw's term
+    float rr = 0.f, back = 0.f;
+    auto factors = [&](float a, float d) {
+      rr = rsqrtf(fmaf(a, inv_group, p.eps));
+      back = -(rr * rr * rr) * (d * inv_group);
+    };
+    if (kWide) factors(sq[0], dot[0]);
 #pragma unroll
     for (int r = 0; r < V; ++r) {
       if (li + span * r < nv) {
-        // dx = (u r) w - x r^3 mean(x u w); (u r) x is dw's term
-        const float rr = rsqrtf(fmaf(sq[kWide ? 0 : r], inv_group, p.eps));
-        const float back = -(rr * rr * rr) * (dot[kWide ? 0 : r] * inv_group);
+        if (!kWide) factors(sq[kWide ? 0 : r], dot[kWide ? 0 : r]);
         const uint32_t xs[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
         float* dwr = dw[kWide ? r : 0];
         weights(r);
@@ -291,14 +311,14 @@ __global__ void __launch_bounds__(norm_bwd_threads(V), 1)
         dst[span * r] = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
-    dst += dst_step;
+    dst += mine.row_step / 8;
     par ^= 1;
     if (++st == p.stages) { st = 0; phase ^= 1u; }
   }
   // No copy may still be landing in shared memory when the CTA exits (only
   // when a wait above ran out can tokens k .. issued-1 still be in flight).
   if (li == 0)
-    for (int k2 = k; k2 < issued; ++k2)
+    for (int k2 = k; k2 < min(issued, my); ++k2)
       mbar_drain_site(&full[k2 % p.stages], (uint32_t)((k2 / p.stages) & 1), kSiteNormBwdDrain);
   if (!__syncthreads_and(k == my) || p.parts == nullptr) return;
   float* out = p.parts + ((long long)tensor * kNormBwdMaxCtas + blockIdx.x) * p.group;

@@ -418,7 +418,7 @@ int launch_block_sparse_bwd(const void* q, const void* k, const void* v, const v
 template <int V>
 int launch_norm_rope_bwd(bool wide, NormBwdParams p, const RopeShape& s, long long tab, int* parts,
                          cudaStream_t stream) {
-  constexpr int kMost = 220 * 1024;                      // dynamic shared memory, beside some 6 KB of static
+  constexpr int kMost = 218 * 1024;                      // dynamic shared memory, beside some 8 KB of static
   static bool done_n[kMaxDevices] = {}, done_w[kMaxDevices] = {};
   static std::mutex mu;
   auto kernel = wide ? bwd_qk_norm_rope3d_kernel<true, V> : bwd_qk_norm_rope3d_kernel<false, V>;
@@ -440,7 +440,7 @@ int launch_norm_rope_bwd(bool wide, NormBwdParams p, const RopeShape& s, long lo
   if (G > enough) G = (int)enough;
   auto stages_of = [&](int g) { return ((kMost - shared) / g - pair_rows) / stage; };
   while (G > 1 && stages_of(G) < 2) --G;
-  long long stages = stages_of(G);                       // at least 3: 124 KB over a 32 KB stage
+  long long stages = stages_of(G);                       // at least 3: 122 KB over a 32 KB stage
   if (stages > kNormBwdMaxStages) stages = kNormBwdMaxStages;
   p.groups = G;
   p.stages = (int)stages;
