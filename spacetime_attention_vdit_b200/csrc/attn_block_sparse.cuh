@@ -69,14 +69,22 @@ struct BitWalk {
   uint32_t bits;   // its bits not yet walked
 };
 
-// One mask row (n bytes, `stride` bytes apart) as bit words, by one warp per word.
+// One mask row (n bytes, `stride` bytes apart) as bit words, a word per warp in
+// turn, four words' loads in flight.
 __device__ __forceinline__ void mask_words(uint32_t* words, const uint8_t* row, long long stride, int n, int warp,
                                            int nwarps, int lane) {
-  for (int w = warp; w * 32 < n; w += nwarps) {
-    const int i = w * 32 + lane;
-    const bool on = i < n && row[i * stride] != 0;
-    const uint32_t m = __ballot_sync(0xffffffffu, on);
-    if (lane == 0) words[w] = m;
+  for (int w0 = warp; w0 * 32 < n; w0 += 4 * nwarps) {
+    bool on[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = (w0 + u * nwarps) * 32 + lane;
+      on[u] = i < n && __ldg(row + i * stride) != 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t m = __ballot_sync(0xffffffffu, on[u]);
+      if (lane == 0 && (w0 + u * nwarps) * 32 < n) words[w0 + u * nwarps] = m;
+    }
   }
 }
 

@@ -28,8 +28,6 @@
 namespace vdit {
 
 struct SparseBwdParams {
-  const __nv_bfloat16* o;
-  const __nv_bfloat16* d_o;
   const float* lse;        // [B, heads, Lq], natural log
   float* stats;            // [2][B * heads][nqb * 128]: lse in log2 units (+inf where no key counts), then delta
   const uint8_t* blocks;   // [B, heads, nqb, nkb]
@@ -142,6 +140,7 @@ __global__ void __launch_bounds__(384, 1)
     grad_attn_fwd_tcgen05_sparse_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
                                            const __grid_constant__ CUtensorMap tmK,
                                            const __grid_constant__ CUtensorMap tmV,
+                                           const __grid_constant__ CUtensorMap tmO,
                                            const __grid_constant__ CUtensorMap tmDO,
                                            const __grid_constant__ CUtensorMap tmDQ, const SparseBwdParams p) {
   using C = SparseBwdCfg<D>;
@@ -182,9 +181,10 @@ __global__ void __launch_bounds__(384, 1)
     mbar_init(ds_ready, 8);              // one elected lane per elementwise warp
     mbar_init(drain, 1);
     fence_mbar_init();
-    mbar_arrive_expect_tx(in_full, 2 * C::TILE_BYTES);
+    mbar_arrive_expect_tx(in_full, 3 * C::TILE_BYTES);
     bwd_load_tile<D>(sQ, &tmQ, in_full, h, q0, b);
     bwd_load_tile<D>(sDO, &tmDO, in_full, h, q0, b);
+    bwd_load_tile<D>(sK + (C::NA - 1) * C::TILE_BYTES, &tmO, in_full, h, q0, b);
   }
   mask_words(bits, p.blocks + ((long long)bh * p.nqb + qb) * p.nkb, 1, p.nkb, warp, 12, lane);
   if (warp == C::MMA_WARP) {
@@ -213,7 +213,9 @@ __global__ void __launch_bounds__(384, 1)
           const int kb = word * 32 + __ffs(left) - 1;
           left &= left - 1u;
           const int sk = x % C::NA, sv = x % C::NB;
-          if (x >= C::NA) ok = mbar_wait(&k_empty[sk], ((x / C::NA) - 1) & 1, kSiteBwdRowFree);
+          // the last stage holds O first, which the elementwise warps release
+          if (sk == C::NA - 1) ok = mbar_wait(&k_empty[sk], (x / C::NA) & 1, kSiteBwdRowFree);
+          else if (x >= C::NA) ok = mbar_wait(&k_empty[sk], ((x / C::NA) - 1) & 1, kSiteBwdRowFree);
           if (!ok) break;
           mbar_arrive_expect_tx(&k_full[sk], C::TILE_BYTES);
           bwd_load_tile<D>(sK + sk * C::TILE_BYTES, &tmK, &k_full[sk], h, kb * C::BN, b);
@@ -277,43 +279,42 @@ __global__ void __launch_bounds__(384, 1)
     const int row = quad * 32 + lane;
     const int i = q0 + row;
     const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
-    // delta of the row: this thread's half of the channels, then the halves' sum
-    float nlse = -INFINITY, ndelta;                      // -lse in log2 units, -delta
+    // Delta of the row, from the tiles of O and dO in shared memory: this thread's
+    // half of the channels, then the halves' sum.  (From global memory, a row per
+    // thread, it took 6 us of a CTA's 27 at 12 key blocks and head_dim 128.)
+    float l = i < p.Lq ? __ldg(p.lse + (long long)bh * p.Lq + i) : -INFINITY;
+    bool ok = warp_wait(in_full, 0, kSiteBwdIn);
     {
       float a = 0.f;
-      if (i < p.Lq) {
-        const long long at = (((long long)b * p.Lq + i) * p.heads + h) * D + half * (D / 2);
-        const uint4* po = reinterpret_cast<const uint4*>(p.o + at);
-        const uint4* pg = reinterpret_cast<const uint4*>(p.d_o + at);
+      const unsigned char* tO = sK + (C::NA - 1) * C::TILE_BYTES;
+      const int key = C::ROWB == 128 ? (row & 7) : ((row >> 1) & 3);
+      constexpr int CPB = C::ROWB / 16;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const uint4 x = __ldg(po + c), y = __ldg(pg + c);
-          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+      for (int c = 0; c < D / 16; ++c) {
+        const int cc = half * (D / 16) + c;
+        const int off = (cc / CPB) * C::DB_BYTES + row * C::ROWB + (((cc % CPB) ^ key) << 4);
+        const uint4 x = *reinterpret_cast<const uint4*>(tO + off), y = *reinterpret_cast<const uint4*>(sDO + off);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const __nv_bfloat162 u = *reinterpret_cast<const __nv_bfloat162*>(&xs[m]);
-            const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&ys[m]);
-            a = fmaf(__low2float(u), __low2float(v), a);
-            a = fmaf(__high2float(u), __high2float(v), a);
-          }
+        for (int m = 0; m < 4; ++m) {
+          a = fmaf(__uint_as_float(xs[m] << 16), __uint_as_float(ys[m] << 16), a);
+          a = fmaf(__uint_as_float(xs[m] & 0xffff0000u), __uint_as_float(ys[m] & 0xffff0000u), a);
         }
-        const float l = __ldg(p.lse + (long long)bh * p.Lq + i);
-        // a row without keys (lse = -inf) gets P = 0, as a row past the sequence
-        if (l != -INFINITY) nlse = -l * 1.4426950408889634f;
       }
       part[half * 128 + row] = a;
-      named_bar_sync(1, 256);
-      const float delta = part[row] + part[128 + row];
-      ndelta = -delta;
-      const long long at = (long long)bh * p.nqb * 128 + q0 + row;
-      p.stats[(half ? p.stats_n : 0) + at] = half ? delta : -nlse;
     }
+    // every warp comes here, also one whose wait ran out
+    named_bar_sync(1, 256);
+    if (threadIdx.x == 0) mbar_arrive(&k_empty[C::NA - 1]);
+    const float delta = part[row] + part[128 + row], ndelta = -delta;
+    // -lse in log2 units; a row without keys (lse = -inf) gets P = 0, as a row past the sequence
+    const float nlse = l != -INFINITY ? -l * 1.4426950408889634f : -INFINITY;
+    p.stats[(half ? p.stats_n : 0) + (long long)bh * p.nqb * 128 + q0 + row] = half ? delta : -nlse;
     const int last = p.nkb - 1, tail_keys = p.Lk - last * C::BN;
     const bool tail = tail_keys < C::BN && ((bits[last >> 5] >> (last & 31)) & 1u) != 0u;
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nlse, nlse),
                  nd2 = make_float2(ndelta, ndelta);
-    bool ok = true;
-    for (int j = 0; j < n; ++j) {
+    for (int j = 0; j < n && ok; ++j) {
       ok = warp_wait(&s_full[j & 1], (j >> 1) & 1, kSiteBwdS);
       if (!ok) break;
       tc_fence_after();
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(384, 1)
       if (lane == 0) mbar_arrive(ds_ready);
     }
     // dQ, scaled once, leaves through the Q buffer (every UMMA has finished)
-    if (ok) ok = n > 0 ? warp_wait(drain, 0, kSiteBwdDone) : warp_wait(in_full, 0, kSiteBwdIn);
+    if (ok && n > 0) ok = warp_wait(drain, 0, kSiteBwdDone);
     if (ok) {
       tc_fence_after();
 #pragma unroll

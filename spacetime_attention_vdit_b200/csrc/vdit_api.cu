@@ -388,14 +388,12 @@ int launch_block_sparse_bwd(const void* q, const void* k, const void* v, const v
       return VDIT_ERR_CUDA;
   }
   const long long tok = (long long)heads * D;
-  CUtensorMap mq, mk, mv, mg, mdq, mdk, mdv;
-  const struct { CUtensorMap* map; const void* at; int L; } maps[7] = {
-      {&mq, q, Lq}, {&mk, k, Lk}, {&mv, v, Lk}, {&mg, d_o, Lq}, {&mdq, dq, Lq}, {&mdk, dk, Lk}, {&mdv, dv, Lk}};
+  CUtensorMap mq, mk, mv, mo, mg, mdq, mdk, mdv;
+  const struct { CUtensorMap* map; const void* at; int L; } maps[8] = {
+      {&mq, q, Lq}, {&mk, k, Lk}, {&mv, v, Lk}, {&mo, o, Lq}, {&mg, d_o, Lq}, {&mdq, dq, Lq}, {&mdk, dk, Lk}, {&mdv, dv, Lk}};
   for (const auto& m : maps)
     if (!make_qkv_map(m.map, m.at, D, heads, 1, m.L, B, tok, tok, tok * m.L)) return VDIT_ERR_CUDA;
   SparseBwdParams p{};
-  p.o = static_cast<const __nv_bfloat16*>(o);
-  p.d_o = static_cast<const __nv_bfloat16*>(d_o);
   p.lse = lse;
   p.stats = stats;
   p.blocks = static_cast<const uint8_t*>(blocks);
@@ -406,7 +404,7 @@ int launch_block_sparse_bwd(const void* q, const void* k, const void* v, const v
   p.scale_log2 = scale * 1.4426950408889634f;
   const long long gq = (long long)B * heads * p.nqb, gk = (long long)B * heads * p.nkb;
   if (gq > 0x7fffffffLL || gk > 0x7fffffffLL) return VDIT_ERR_SHAPE;
-  grad_attn_fwd_tcgen05_sparse_dq_kernel<D><<<(unsigned)gq, C::THREADS, C::DQ_SMEM, stream>>>(mq, mk, mv, mg, mdq, p);
+  grad_attn_fwd_tcgen05_sparse_dq_kernel<D><<<(unsigned)gq, C::THREADS, C::DQ_SMEM, stream>>>(mq, mk, mv, mo, mg, mdq, p);
   const int rc = last_launch_status();
   if (rc != VDIT_OK) return rc;
   grad_attn_fwd_tcgen05_sparse_dkv_kernel<D><<<(unsigned)gk, C::THREADS, C::DKV_SMEM, stream>>>(mq, mk, mv, mg, mdk,
