@@ -51,6 +51,9 @@ struct SparseParams {
 template <int D>
 struct SparseCfg : AttnCfg<D> {
   using A = AttnCfg<D>;
+  // more registers for the issuing thread than the dense kernel's (+1 %)
+  static constexpr int REGS_SOFT = 208, REGS_CTRL = 88;
+  static_assert(2 * 128 * REGS_SOFT + 128 * REGS_CTRL <= A::THREADS * A::REGS_LAUNCH, "register split");
   static constexpr int NBARS = 1 + 2 * A::NK + 2 * A::NV + 3 * A::NQ + 1;
   static constexpr int BITS_OFF = (A::NQ + A::NK + A::NV) * A::TILE_BYTES;
   static constexpr int BARS_OFF = BITS_OFF + A::NQ * kSparseWords * 4;
@@ -85,6 +88,60 @@ __device__ __forceinline__ void mask_words(uint32_t* words, const uint8_t* row, 
       const uint32_t m = __ballot_sync(0xffffffffu, on[u]);
       if (lane == 0 && (w0 + u * nwarps) * 32 < n) words[w0 + u * nwarps] = m;
     }
+  }
+}
+
+// ---- UMMAs from precomputed descriptors
+//
+// One thread issues every UMMA, and at 16 per tile step what it computes for each
+// weighs: building both 64-bit descriptors from addresses every time took longer
+// than the tensor core needs for the products.  The words of a descriptor are
+// built once per operand; a UMMA's own is an addition to the address field of the
+// low word (14 bits of 16 bytes: shared memory never carries out of it).
+
+struct UmmaDesc {
+  uint32_t lo, hi;
+  __device__ __forceinline__ UmmaDesc(const void* at, uint32_t lbo_bytes, uint32_t sbo_bytes, uint32_t swizzle) {
+    const uint64_t d = umma_sdesc(smem_u32(at), lbo_bytes, sbo_bytes, swizzle);
+    lo = (uint32_t)d;
+    hi = (uint32_t)(d >> 32);
+  }
+};
+
+// D[tmem] (+)= A[smem] * B[smem], operands `a` and `b` bytes behind their descriptors.
+template <bool kAccumulate>
+__device__ __forceinline__ void umma_ss_at(uint32_t d, const UmmaDesc& da, uint32_t a, const UmmaDesc& db, uint32_t b,
+                                           uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+      "r"(da.lo + (a >> 4)), "r"(da.hi), "r"(db.lo + (b >> 4)), "r"(db.hi), "r"(idesc), "n"(kAccumulate ? 1 : 0)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem].
+__device__ __forceinline__ void umma_ts_at(uint32_t d, uint32_t a, const UmmaDesc& db, uint32_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(db.lo + (b >> 4)), "r"(db.hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// One 128 x 128 product of two K-major tiles of D columns, `a` and `b` bytes
+// behind the descriptors of their buffers.
+template <int D>
+__device__ __forceinline__ void umma_scores(uint32_t acc, const UmmaDesc& da, uint32_t a, const UmmaDesc& db,
+                                            uint32_t b) {
+  using C = AttnCfg<D>;
+  umma_ss_at<false>(acc, da, a, db, b, C::IDESC_QK);
+#pragma unroll
+  for (int kk = 1; kk < D / 16; ++kk) {
+    const uint32_t off = (kk / (C::DBLK / 16)) * C::DB_BYTES + (kk % (C::DBLK / 16)) * 32;
+    umma_ss_at<true>(acc, da, a + off, db, b + off, C::IDESC_QK);
   }
 }
 
@@ -235,7 +292,7 @@ __global__ void __launch_bounds__(384, 1)
   const int steps0 = n_both + n_own0, steps1 = n_both + n_own1;   // key tiles of tile 0 and of tile 1
 
   if (warp >= 8) {
-    regs_decrease<C::REGS_CONTROL>();
+    regs_decrease<C::REGS_CTRL>();
     if (warp == C::TMA_WARP) {
       // ---------------------------------------------------------------- TMA
       if (lane == 0) {
@@ -304,28 +361,19 @@ __global__ void __launch_bounds__(384, 1)
     } else if (warp == C::MMA_WARP) {
       // ---------------------------------------------------------------- MMA
       if (lane == 0) {
-        const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV);
         constexpr uint32_t SBO = 8 * C::ROWB;       // 8-row core-matrix group stride
+        const UmmaDesc dQ(sQ, 16, SBO, C::SWZ), dK(sK, 16, SBO, C::SWZ), dV(sV, C::DB_BYTES, SBO, C::SWZ);
         int ki = 0, vi = 0;                         // K and V items consumed so far
         auto qk = [&](int i) {
-          const int st = ki % C::NK;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk / (C::DBLK / 16)) * C::DB_BYTES + (kk % (C::DBLK / 16)) * 32;
-            const uint64_t a = umma_sdesc(sQa + i * C::TILE_BYTES + off, 16, SBO, C::SWZ);
-            const uint64_t bd = umma_sdesc(sKa + st * C::TILE_BYTES + off, 16, SBO, C::SWZ);
-            umma_ss(tmem + C::S_COL + i * C::BN, a, bd, C::IDESC_QK, kk > 0 ? 1u : 0u);
-          }
+          umma_scores<D>(tmem + C::S_COL + i * C::BN, dQ, i * C::TILE_BYTES, dK, (ki % C::NK) * C::TILE_BYTES);
           umma_commit(&s_full[i]);
         };
         auto pv = [&](int i, bool first) {
-          const int st = vi % C::NV;
+          const uint32_t st = (vi % C::NV) * C::TILE_BYTES;
 #pragma unroll
-          for (int kk = 0; kk < C::BN / 16; ++kk) {
-            const uint64_t bd = umma_sdesc(sVa + st * C::TILE_BYTES + kk * 16 * C::ROWB, C::DB_BYTES, SBO, C::SWZ);
-            umma_ts(tmem + C::O_COL + i * C::BM, tmem + C::S_COL + i * C::BN + kk * 8, bd, C::IDESC_PV,
-                    (!first || kk > 0) ? 1u : 0u);
-          }
+          for (int kk = 0; kk < C::BN / 16; ++kk)
+            umma_ts_at(tmem + C::O_COL + i * C::BM, tmem + C::S_COL + i * C::BN + kk * 8, dV, st + kk * 16 * C::ROWB,
+                       C::IDESC_PV, (!first || kk > 0) ? 1u : 0u);
         };
         // Step j of tile i takes its j-th key tile.  Of a tile that serves
         // both, tile 0's product waits for the copy and tile 1's releases it.
@@ -353,8 +401,9 @@ __global__ void __launch_bounds__(384, 1)
             tc_fence_after();
             pv(i, j == 0);
             if (j + 1 == mine) umma_commit(&o_done[i]);
-            if (!shared || i == 1) { umma_commit(&v_empty[vi % C::NV]); ++vi; }
             if (j + 1 < mine) ok = scores(i, j + 1);
+            // behind Q.K^T, which P.V's tail would else have to leave the pipe for
+            if (!shared || i == 1) { umma_commit(&v_empty[vi % C::NV]); ++vi; }
           }
         }
         // every UMMA issued above has finished before TMEM is released
@@ -364,7 +413,7 @@ __global__ void __launch_bounds__(384, 1)
       __syncwarp();
     }
   } else {
-    regs_increase<C::REGS_SOFTMAX>();
+    regs_increase<C::REGS_SOFT>();
     // -------------------------------------------------------------- softmax
     const int tile = warp >> 2;                   // warps 0..3 -> tile 0, 4..7 -> tile 1
     const int quad = warp & 3;                    // TMEM lanes this warp may touch

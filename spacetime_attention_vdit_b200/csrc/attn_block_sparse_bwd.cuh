@@ -44,6 +44,9 @@ enum : int {
 template <int D>
 struct SparseBwdCfg : AttnCfg<D> {
   using A = AttnCfg<D>;
+  // registers: at the dense kernel's 56 the issuing thread spills
+  static constexpr int REGS_ELEMENT = 208, REGS_CTRL = 88;
+  static_assert(2 * 128 * REGS_ELEMENT + 128 * REGS_CTRL <= A::THREADS * A::REGS_LAUNCH, "register split");
   // dq: Q and dO stay, K and V stream (K is needed once more, for dQ, after V)
   static constexpr int NA = 3, NB = 2;
   static constexpr int TILES = 2 + NA + NB;
@@ -64,29 +67,17 @@ struct SparseBwdCfg : AttnCfg<D> {
   static constexpr uint32_t KV_S = 0, KV_DP = 128, KV_DV = 256, KV_DK = 384;
 };
 
-// One 128 x 128 product, both operands K-major tiles of D columns in shared memory.
-template <int D>
-__device__ __forceinline__ void bwd_scores(uint32_t acc, uint32_t a_tile, uint32_t b_tile) {
-  using C = AttnCfg<D>;
-#pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
-    const uint32_t off = (kk / (C::DBLK / 16)) * C::DB_BYTES + (kk % (C::DBLK / 16)) * 32;
-    umma_ss(acc, umma_sdesc(a_tile + off, 16, 8 * C::ROWB, C::SWZ), umma_sdesc(b_tile + off, 16, 8 * C::ROWB, C::SWZ),
-            C::IDESC_QK, kk > 0 ? 1u : 0u);
-  }
-}
-
 // acc [128 x D] += A [128 x 128, bf16 in TMEM] * B [128 rows of D, MN-major in
-// shared memory].  A's packed columns: the first 64 of its columns at a, the
-// others 64 TMEM columns further (each warpgroup packs over its own scores).
+// shared memory, `b` bytes behind the descriptor].  A's packed columns: the first 64
+// of its columns at a, the others 64 TMEM columns further (each warpgroup packs over
+// its own scores).
 template <int D>
-__device__ __forceinline__ void bwd_accumulate(uint32_t acc, uint32_t a, uint32_t b_tile, bool first) {
+__device__ __forceinline__ void bwd_accumulate(uint32_t acc, uint32_t a, const UmmaDesc& db, uint32_t b, bool first) {
   using C = AttnCfg<D>;
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk)
-    umma_ts(acc, a + (kk >> 2) * 64 + (kk & 3) * 8,
-            umma_sdesc(b_tile + kk * 16 * C::ROWB, C::DB_BYTES, 8 * C::ROWB, C::SWZ), C::IDESC_PV,
-            (!first || kk > 0) ? 1u : 0u);
+    umma_ts_at(acc, a + (kk >> 2) * 64 + (kk & 3) * 8, db, b + kk * 16 * C::ROWB, C::IDESC_PV,
+               (!first || kk > 0) ? 1u : 0u);
 }
 
 // Load one 128-row tile of (head h, batch b) starting at token `row`.
@@ -201,7 +192,7 @@ __global__ void __launch_bounds__(384, 1)
   n = warp_sum(n);
 
   if (warp >= 8) {
-    regs_decrease<C::REGS_CONTROL>();
+    regs_decrease<C::REGS_CTRL>();
     if (warp == C::TMA_WARP) {
       if (lane == 0) {
         int word = -1;
@@ -235,18 +226,20 @@ __global__ void __launch_bounds__(384, 1)
       }
     } else if (warp == C::MMA_WARP) {
       if (lane == 0) {
-        const uint32_t sQa = smem_u32(sQ), sDOa = smem_u32(sDO), sKa = smem_u32(sK), sVa = smem_u32(sV);
+        constexpr uint32_t SBO = 8 * C::ROWB;
+        const UmmaDesc dQ(sQ, 16, SBO, C::SWZ), dG(sDO, 16, SBO, C::SWZ), dK(sK, 16, SBO, C::SWZ),
+            dV(sV, 16, SBO, C::SWZ), dKt(sK, C::DB_BYTES, SBO, C::SWZ);
         auto scores = [&](int j) -> bool {               // S_j = Q K_j^T
           if (!mbar_wait(&k_full[j % C::NA], (j / C::NA) & 1, kSiteBwdRow)) return false;
           tc_fence_after();
-          bwd_scores<D>(tmem + C::DQ_S + (j & 1) * 128, sQa, sKa + (j % C::NA) * C::TILE_BYTES);
+          umma_scores<D>(tmem + C::DQ_S + (j & 1) * 128, dQ, 0, dK, (j % C::NA) * C::TILE_BYTES);
           umma_commit(&s_full[j & 1]);
           return true;
         };
         auto dprob = [&](int j) -> bool {                // dP_j = dO V_j^T
           if (!mbar_wait(&v_full[j % C::NB], (j / C::NB) & 1, kSiteBwdCol)) return false;
           tc_fence_after();
-          bwd_scores<D>(tmem + C::DQ_DP, sDOa, sVa + (j % C::NB) * C::TILE_BYTES);
+          umma_scores<D>(tmem + C::DQ_DP, dG, 0, dV, (j % C::NB) * C::TILE_BYTES);
           umma_commit(dp_full);
           umma_commit(&v_empty[j % C::NB]);
           return true;
@@ -260,7 +253,7 @@ __global__ void __launch_bounds__(384, 1)
           tc_fence_after();
           if (j + 1 < n) ok = dprob(j + 1);
           if (!ok) break;
-          bwd_accumulate<D>(tmem + C::DQ_ACC, tmem + C::DQ_S + (j & 1) * 128, sKa + (j % C::NA) * C::TILE_BYTES,
+          bwd_accumulate<D>(tmem + C::DQ_ACC, tmem + C::DQ_S + (j & 1) * 128, dKt, (j % C::NA) * C::TILE_BYTES,
                             j == 0);
           umma_commit(&k_empty[j % C::NA]);
           // S_{j+2} takes the columns dQ's product above reads: UMMAs of one
@@ -273,7 +266,7 @@ __global__ void __launch_bounds__(384, 1)
       __syncwarp();
     }
   } else {
-    regs_increase<C::REGS_SOFTMAX>();
+    regs_increase<C::REGS_ELEMENT>();
     const int half = warp >> 2;                          // columns 64 half .. 64 half + 63
     const int quad = warp & 3;
     const int row = quad * 32 + lane;
@@ -480,7 +473,7 @@ __global__ void __launch_bounds__(384, 1)
   n = warp_sum(n);
 
   if (warp >= 8) {
-    regs_decrease<C::REGS_CONTROL>();
+    regs_decrease<C::REGS_CTRL>();
     if (warp == C::TMA_WARP) {
       if (lane == 0) {
         int word = -1;
@@ -520,18 +513,20 @@ __global__ void __launch_bounds__(384, 1)
       }
     } else if (warp == C::MMA_WARP) {
       if (lane == 0) {
-        const uint32_t sQa = smem_u32(sQ), sDOa = smem_u32(sDO), sKa = smem_u32(sK), sVa = smem_u32(sV);
+        constexpr uint32_t SBO = 8 * C::ROWB;
+        const UmmaDesc dK(sK, 16, SBO, C::SWZ), dV(sV, 16, SBO, C::SWZ), dQ(sQ, 16, SBO, C::SWZ),
+            dG(sDO, 16, SBO, C::SWZ), dQt(sQ, C::DB_BYTES, SBO, C::SWZ), dGt(sDO, C::DB_BYTES, SBO, C::SWZ);
         auto scores = [&](int j) -> bool {               // S_j^T = K Q_j^T
           if (!mbar_wait(&q_full[j % C::NA], (j / C::NA) & 1, kSiteBwdRow)) return false;
           tc_fence_after();
-          bwd_scores<D>(tmem + C::KV_S, sKa, sQa + (j % C::NA) * C::TILE_BYTES);
+          umma_scores<D>(tmem + C::KV_S, dK, 0, dQ, (j % C::NA) * C::TILE_BYTES);
           umma_commit(s_full);
           return true;
         };
         auto dprob = [&](int j) -> bool {                // dP_j^T = V dO_j^T
           if (!mbar_wait(&do_full[j % C::NB], (j / C::NB) & 1, kSiteBwdCol)) return false;
           tc_fence_after();
-          bwd_scores<D>(tmem + C::KV_DP, sVa, sDOa + (j % C::NB) * C::TILE_BYTES);
+          umma_scores<D>(tmem + C::KV_DP, dV, 0, dG, (j % C::NB) * C::TILE_BYTES);
           umma_commit(dp_full);
           return true;
         };
@@ -541,7 +536,7 @@ __global__ void __launch_bounds__(384, 1)
           ok = mbar_wait(p_ready, j & 1, kSiteBwdP);
           if (!ok) break;
           tc_fence_after();
-          bwd_accumulate<D>(tmem + C::KV_DV, tmem + C::KV_S, sDOa + (j % C::NB) * C::TILE_BYTES, j == 0);
+          bwd_accumulate<D>(tmem + C::KV_DV, tmem + C::KV_S, dGt, (j % C::NB) * C::TILE_BYTES, j == 0);
           umma_commit(&do_empty[j % C::NB]);
           // S_{j+1} takes the columns of P_j, dP_{j+1} those of dS_j: UMMAs of
           // one thread execute in issue order
@@ -549,7 +544,7 @@ __global__ void __launch_bounds__(384, 1)
           if (ok) ok = mbar_wait(ds_ready, j & 1, kSiteBwdDs);
           if (!ok) break;
           tc_fence_after();
-          bwd_accumulate<D>(tmem + C::KV_DK, tmem + C::KV_DP, sQa + (j % C::NA) * C::TILE_BYTES, j == 0);
+          bwd_accumulate<D>(tmem + C::KV_DK, tmem + C::KV_DP, dQt, (j % C::NA) * C::TILE_BYTES, j == 0);
           umma_commit(&q_empty[j % C::NA]);
           if (j + 1 < n) ok = dprob(j + 1);
         }
@@ -559,7 +554,7 @@ __global__ void __launch_bounds__(384, 1)
       __syncwarp();
     }
   } else {
-    regs_increase<C::REGS_SOFTMAX>();
+    regs_increase<C::REGS_ELEMENT>();
     const int half = warp >> 2;                          // columns (queries) 64 half .. 64 half + 63
     const int quad = warp & 3;
     const int row = quad * 32 + lane;                    // key within the block
