@@ -145,6 +145,16 @@ __device__ __forceinline__ void umma_scores(uint32_t acc, const UmmaDesc& da, ui
   }
 }
 
+// A ring's stage and the parity of its barriers.
+template <int N>
+struct RingPos {
+  int st = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++st == N) { st = 0; phase ^= 1u; }
+  }
+};
+
 // ---- thread-block clusters and distributed shared memory
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -363,49 +373,48 @@ __global__ void __launch_bounds__(384, 1)
       if (lane == 0) {
         constexpr uint32_t SBO = 8 * C::ROWB;       // 8-row core-matrix group stride
         const UmmaDesc dQ(sQ, 16, SBO, C::SWZ), dK(sK, 16, SBO, C::SWZ), dV(sV, C::DB_BYTES, SBO, C::SWZ);
-        int ki = 0, vi = 0;                         // K and V items consumed so far
-        auto qk = [&](int i) {
-          umma_scores<D>(tmem + C::S_COL + i * C::BN, dQ, i * C::TILE_BYTES, dK, (ki % C::NK) * C::TILE_BYTES);
-          umma_commit(&s_full[i]);
-        };
-        auto pv = [&](int i, bool first) {
-          const uint32_t st = (vi % C::NV) * C::TILE_BYTES;
-#pragma unroll
-          for (int kk = 0; kk < C::BN / 16; ++kk)
-            umma_ts_at(tmem + C::O_COL + i * C::BM, tmem + C::S_COL + i * C::BN + kk * 8, dV, st + kk * 16 * C::ROWB,
-                       C::IDESC_PV, (!first || kk > 0) ? 1u : 0u);
-        };
+        RingPos<C::NK> kr;                          // K and V items consumed so far
+        RingPos<C::NV> vr;
         // Step j of tile i takes its j-th key tile.  Of a tile that serves
         // both, tile 0's product waits for the copy and tile 1's releases it.
-        auto scores = [&](int i, int j) -> bool {
+        auto scores = [&](auto tile, int j) -> bool {
+          constexpr int i = decltype(tile)::value;
           const bool shared = j < n_both;
           if (!shared || i == 0)
-            if (!mbar_wait(&k_full[ki % C::NK], (ki / C::NK) & 1, kSiteKFull)) return false;
+            if (!mbar_wait(&k_full[kr.st], kr.phase, kSiteKFull)) return false;
           tc_fence_after();
-          qk(i);
-          if (!shared || i == 1) { umma_commit(&k_empty[ki % C::NK]); ++ki; }
+          umma_scores<D>(tmem + C::S_COL + i * C::BN, dQ, i * C::TILE_BYTES, dK, kr.st * C::TILE_BYTES);
+          umma_commit(&s_full[i]);
+          if (!shared || i == 1) { umma_commit(&k_empty[kr.st]); kr.step(); }
           return true;
         };
+        auto turn = [&](auto tile, int j) -> bool {     // O_i += P_i V of step j, then S_i of step j + 1
+          constexpr int i = decltype(tile)::value;
+          const int mine = i == 0 ? steps0 : steps1;
+          if (j >= mine) return true;
+          const bool shared = j < n_both;
+          if (!shared || i == 0)
+            if (!mbar_wait(&v_full[vr.st], vr.phase, kSiteVFull)) return false;
+          if (!mbar_wait(&p_full[i], j & 1, kSitePFull)) return false;
+          tc_fence_after();
+          const uint32_t v_at = vr.st * C::TILE_BYTES;
+          umma_ts_at(tmem + C::O_COL + i * C::BM, tmem + C::S_COL + i * C::BN, dV, v_at, C::IDESC_PV, j > 0 ? 1u : 0u);
+#pragma unroll
+          for (int kk = 1; kk < C::BN / 16; ++kk)
+            umma_ts_at(tmem + C::O_COL + i * C::BM, tmem + C::S_COL + i * C::BN + kk * 8, dV, v_at + kk * 16 * C::ROWB,
+                       C::IDESC_PV, 1u);
+          if (j + 1 == mine) umma_commit(&o_done[i]);
+          if (j + 1 < mine && !scores(tile, j + 1)) return false;
+          if (!shared || i == 1) { umma_commit(&v_empty[vr.st]); vr.step(); }
+          return true;
+        };
+        constexpr std::integral_constant<int, 0> tile0{};
+        constexpr std::integral_constant<int, 1> tile1{};
         bool ok = mbar_wait(q_full, 0, kSiteQFull);
-        if (ok && steps0 > 0) ok = scores(0, 0);
-        if (ok && steps1 > 0) ok = scores(1, 0);
+        if (ok && steps0 > 0) ok = scores(tile0, 0);
+        if (ok && steps1 > 0) ok = scores(tile1, 0);
         const int steps = max(steps0, steps1);
-        for (int j = 0; j < steps && ok; ++j) {
-          for (int i = 0; i < 2 && ok; ++i) {
-            const int mine = i == 0 ? steps0 : steps1;
-            if (j >= mine) continue;
-            const bool shared = j < n_both;
-            if (!shared || i == 0) ok = mbar_wait(&v_full[vi % C::NV], (vi / C::NV) & 1, kSiteVFull);
-            if (ok) ok = mbar_wait(&p_full[i], j & 1, kSitePFull);
-            if (!ok) break;
-            tc_fence_after();
-            pv(i, j == 0);
-            if (j + 1 == mine) umma_commit(&o_done[i]);
-            if (j + 1 < mine) ok = scores(i, j + 1);
-            // behind Q.K^T, which P.V's tail would else have to leave the pipe for
-            if (!shared || i == 1) { umma_commit(&v_empty[vi % C::NV]); ++vi; }
-          }
-        }
+        for (int j = 0; j < steps && ok; ++j) ok = turn(tile0, j) && turn(tile1, j);
         // every UMMA issued above has finished before TMEM is released
         umma_commit(drain);
         mbar_drain(drain, 0);

@@ -74,10 +74,10 @@ struct SparseBwdCfg : AttnCfg<D> {
 template <int D>
 __device__ __forceinline__ void bwd_accumulate(uint32_t acc, uint32_t a, const UmmaDesc& db, uint32_t b, bool first) {
   using C = AttnCfg<D>;
+  umma_ts_at(acc, a, db, b, C::IDESC_PV, first ? 0u : 1u);
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    umma_ts_at(acc, a + (kk >> 2) * 64 + (kk & 3) * 8, db, b + kk * 16 * C::ROWB, C::IDESC_PV,
-               (!first || kk > 0) ? 1u : 0u);
+  for (int kk = 1; kk < 8; ++kk)
+    umma_ts_at(acc, a + (kk >> 2) * 64 + (kk & 3) * 8, db, b + kk * 16 * C::ROWB, C::IDESC_PV, 1u);
 }
 
 // Load one 128-row tile of (head h, batch b) starting at token `row`.
@@ -229,36 +229,45 @@ __global__ void __launch_bounds__(384, 1)
         constexpr uint32_t SBO = 8 * C::ROWB;
         const UmmaDesc dQ(sQ, 16, SBO, C::SWZ), dG(sDO, 16, SBO, C::SWZ), dK(sK, 16, SBO, C::SWZ),
             dV(sV, 16, SBO, C::SWZ), dKt(sK, C::DB_BYTES, SBO, C::SWZ);
+        RingPos<C::NA> ks, ka;                           // K: as S's operand, and later as dQ's
+        RingPos<C::NB> vr;
         auto scores = [&](int j) -> bool {               // S_j = Q K_j^T
-          if (!mbar_wait(&k_full[j % C::NA], (j / C::NA) & 1, kSiteBwdRow)) return false;
+          if (!mbar_wait(&k_full[ks.st], ks.phase, kSiteBwdRow)) return false;
           tc_fence_after();
-          umma_scores<D>(tmem + C::DQ_S + (j & 1) * 128, dQ, 0, dK, (j % C::NA) * C::TILE_BYTES);
+          umma_scores<D>(tmem + C::DQ_S + (j & 1) * 128, dQ, 0, dK, ks.st * C::TILE_BYTES);
           umma_commit(&s_full[j & 1]);
+          ks.step();
           return true;
         };
-        auto dprob = [&](int j) -> bool {                // dP_j = dO V_j^T
-          if (!mbar_wait(&v_full[j % C::NB], (j / C::NB) & 1, kSiteBwdCol)) return false;
+        auto dprob = [&]() -> bool {                     // dP_j = dO V_j^T
+          if (!mbar_wait(&v_full[vr.st], vr.phase, kSiteBwdCol)) return false;
           tc_fence_after();
-          umma_scores<D>(tmem + C::DQ_DP, dG, 0, dV, (j % C::NB) * C::TILE_BYTES);
+          umma_scores<D>(tmem + C::DQ_DP, dG, 0, dV, vr.st * C::TILE_BYTES);
           umma_commit(dp_full);
-          umma_commit(&v_empty[j % C::NB]);
+          umma_commit(&v_empty[vr.st]);
+          vr.step();
           return true;
         };
         bool ok = mbar_wait(in_full, 0, kSiteBwdIn);
-        if (ok && n > 0) ok = scores(0) && dprob(0);
+        if (ok && n > 0) ok = scores(0) && dprob();
         if (ok && n > 1) ok = scores(1);
         for (int j = 0; j < n && ok; ++j) {
           ok = mbar_wait(ds_ready, j & 1, kSiteBwdDs);
           if (!ok) break;
           tc_fence_after();
-          if (j + 1 < n) ok = dprob(j + 1);
+          if (j + 1 < n) ok = dprob();
           if (!ok) break;
-          bwd_accumulate<D>(tmem + C::DQ_ACC, tmem + C::DQ_S + (j & 1) * 128, dKt, (j % C::NA) * C::TILE_BYTES,
-                            j == 0);
-          umma_commit(&k_empty[j % C::NA]);
+          bwd_accumulate<D>(tmem + C::DQ_ACC, tmem + C::DQ_S + (j & 1) * 128, dKt, ka.st * C::TILE_BYTES, j == 0);
           // S_{j+2} takes the columns dQ's product above reads: UMMAs of one
           // thread execute in issue order
-          if (j + 2 < n) ok = scores(j + 2);
+          if (j + 2 < n) {
+            const int st = ka.st;
+            ok = scores(j + 2);
+            umma_commit(&k_empty[st]);
+          } else {
+            umma_commit(&k_empty[ka.st]);
+          }
+          ka.step();
         }
         umma_commit(drain);
         mbar_drain(drain, 0);
@@ -516,37 +525,43 @@ __global__ void __launch_bounds__(384, 1)
         constexpr uint32_t SBO = 8 * C::ROWB;
         const UmmaDesc dK(sK, 16, SBO, C::SWZ), dV(sV, 16, SBO, C::SWZ), dQ(sQ, 16, SBO, C::SWZ),
             dG(sDO, 16, SBO, C::SWZ), dQt(sQ, C::DB_BYTES, SBO, C::SWZ), dGt(sDO, C::DB_BYTES, SBO, C::SWZ);
-        auto scores = [&](int j) -> bool {               // S_j^T = K Q_j^T
-          if (!mbar_wait(&q_full[j % C::NA], (j / C::NA) & 1, kSiteBwdRow)) return false;
+        RingPos<C::NA> qs, qa;                           // Q: as S's operand, and later as dK's
+        RingPos<C::NB> gs, ga;                           // dO: as dP's operand, and as dV's
+        auto scores = [&]() -> bool {                    // S_j^T = K Q_j^T
+          if (!mbar_wait(&q_full[qs.st], qs.phase, kSiteBwdRow)) return false;
           tc_fence_after();
-          umma_scores<D>(tmem + C::KV_S, dK, 0, dQ, (j % C::NA) * C::TILE_BYTES);
+          umma_scores<D>(tmem + C::KV_S, dK, 0, dQ, qs.st * C::TILE_BYTES);
           umma_commit(s_full);
+          qs.step();
           return true;
         };
-        auto dprob = [&](int j) -> bool {                // dP_j^T = V dO_j^T
-          if (!mbar_wait(&do_full[j % C::NB], (j / C::NB) & 1, kSiteBwdCol)) return false;
+        auto dprob = [&]() -> bool {                     // dP_j^T = V dO_j^T
+          if (!mbar_wait(&do_full[gs.st], gs.phase, kSiteBwdCol)) return false;
           tc_fence_after();
-          umma_scores<D>(tmem + C::KV_DP, dV, 0, dG, (j % C::NB) * C::TILE_BYTES);
+          umma_scores<D>(tmem + C::KV_DP, dV, 0, dG, gs.st * C::TILE_BYTES);
           umma_commit(dp_full);
+          gs.step();
           return true;
         };
         bool ok = mbar_wait(in_full, 0, kSiteBwdIn);
-        if (ok && n > 0) ok = scores(0) && dprob(0);
+        if (ok && n > 0) ok = scores() && dprob();
         for (int j = 0; j < n && ok; ++j) {
           ok = mbar_wait(p_ready, j & 1, kSiteBwdP);
           if (!ok) break;
           tc_fence_after();
-          bwd_accumulate<D>(tmem + C::KV_DV, tmem + C::KV_S, dGt, (j % C::NB) * C::TILE_BYTES, j == 0);
-          umma_commit(&do_empty[j % C::NB]);
+          bwd_accumulate<D>(tmem + C::KV_DV, tmem + C::KV_S, dGt, ga.st * C::TILE_BYTES, j == 0);
           // S_{j+1} takes the columns of P_j, dP_{j+1} those of dS_j: UMMAs of
           // one thread execute in issue order
-          if (j + 1 < n) ok = scores(j + 1);
+          if (j + 1 < n) ok = scores();
+          umma_commit(&do_empty[ga.st]);
+          ga.step();
           if (ok) ok = mbar_wait(ds_ready, j & 1, kSiteBwdDs);
           if (!ok) break;
           tc_fence_after();
-          bwd_accumulate<D>(tmem + C::KV_DK, tmem + C::KV_DP, dQt, (j % C::NA) * C::TILE_BYTES, j == 0);
-          umma_commit(&q_empty[j % C::NA]);
-          if (j + 1 < n) ok = dprob(j + 1);
+          bwd_accumulate<D>(tmem + C::KV_DK, tmem + C::KV_DP, dQt, qa.st * C::TILE_BYTES, j == 0);
+          if (j + 1 < n) ok = dprob();
+          umma_commit(&q_empty[qa.st]);
+          qa.step();
         }
         umma_commit(drain);
         mbar_drain(drain, 0);
