@@ -35,7 +35,7 @@ __device__ __forceinline__ bool tripped(const unsigned int* flag) {
 }
 
 // Means of every 128-token block of Q (blockIdx.x < nqb) and K: a CTA takes 256
-// channels of one block, a thread 8 channels of every 8th token.  bound by the
+// channels of one block, a thread 8 channels of every 8th token.  Bound by the
 // bytes of Q and K; a conversion instruction to float64 per value would take
 // longer than they do (16 per clock and SM), so a bfloat16's bits are moved into
 // a float64's high word as they are: exponent field e stands for 2^(e - 1023)
@@ -120,11 +120,13 @@ __device__ __forceinline__ unsigned long long order_key(double x) {
   return v < 0 ? ~(unsigned long long)v : (unsigned long long)v | 0x8000000000000000ull;
 }
 
-// Scores of 64 query blocks x 64 key blocks of one head: 64 threads, 8 x 8 each,
+// Scores of 64 query blocks x 64 key blocks of one head: 128 threads, 4 x 8 each,
 // the means fetched 16 channels at a time into two buffers with asynchronous
-// copies (rows of 144 bytes: the eight rows a quarter-warp reads 16 bytes of
-// fall into different banks).  Bound by the float64 units.  The ordered scores
-// leave as two arrays of 32-bit words: the second is hardly ever read.
+// copies (rows of 144 bytes: the eight rows that eight lanes read 16 bytes of fall
+// into different banks).  Bound by issuing float64 multiply-adds (60 % of its
+// instructions; 45 us for 40 x 256 x 256 scores of 128 channels, 35 % of the float64
+// units' rate); 64 threads of 8 x 8 take 4 % longer.  The ordered scores leave as
+// two arrays of 32-bit words: the second is hardly ever read.
 constexpr int kScoreRow = 18;                            // doubles per staged row: 16 channels and padding
 
 __device__ __forceinline__ void copy16(void* dst, const void* src, bool on) {
@@ -132,9 +134,9 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 
-__global__ void __launch_bounds__(64) block_scores_kernel(const double* __restrict__ qm, const double* __restrict__ km,
-                                                          uint32_t* hi, uint32_t* lo, SelectShape s,
-                                                          const unsigned int* flag) {
+__global__ void __launch_bounds__(128, 4) block_scores_kernel(const double* __restrict__ qm,
+                                                              const double* __restrict__ km, uint32_t* hi,
+                                                              uint32_t* lo, SelectShape s, const unsigned int* flag) {
   __shared__ __align__(16) double st[2][2][64 * kScoreRow];
   if (tripped(flag)) return;
   const long long bh = blockIdx.z;
@@ -142,15 +144,15 @@ __global__ void __launch_bounds__(64) block_scores_kernel(const double* __restri
   const int ty = threadIdx.x >> 3, tx = threadIdx.x & 7;
   auto fetch = [&](int buf, int d0) {                    // 2 x 64 rows x 8 chunks of 16 bytes
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const int r = ty + 8 * (c & 7), which = c >> 3;
+    for (int c = 0; c < 8; ++c) {
+      const int r = ty + 16 * (c & 3), which = c >> 2;
       const int row = (which ? j0 : i0) + r, n = which ? s.nkb : s.nqb;
       const double* from = (which ? km : qm) + (bh * n + min(row, n - 1)) * s.D + d0 + tx * 2;
       copy16(&st[buf][which][r * kScoreRow + tx * 2], from, row < n);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  double acc[8][8] = {};
+  double acc[4][8] = {};
   const int steps = s.D / 16;
   fetch(0, 0);
   for (int x = 0; x < steps; ++x) {
@@ -163,30 +165,25 @@ __global__ void __launch_bounds__(64) block_scores_kernel(const double* __restri
     __syncthreads();
     const double* sq = &st[x & 1][0][ty * kScoreRow];
     const double* sk = &st[x & 1][1][tx * kScoreRow];
+#pragma unroll 2
+    for (int d = 0; d < 16; ++d) {
+      double q[4];
 #pragma unroll
-    for (int d = 0; d < 16; d += 2) {
-      double2 q[8], k[8];
+      for (int m = 0; m < 4; ++m) q[m] = sq[16 * m * kScoreRow + d];
 #pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        q[m] = *reinterpret_cast<const double2*>(sq + 8 * m * kScoreRow + d);
-        k[m] = *reinterpret_cast<const double2*>(sk + 8 * m * kScoreRow + d);
+      for (int n = 0; n < 8; ++n) {
+        const double k = sk[8 * n * kScoreRow + d];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) acc[m][n] = fma(q[m], k, acc[m][n]);
       }
-#pragma unroll
-      for (int m = 0; m < 8; ++m)
-#pragma unroll
-        for (int n = 0; n < 8; ++n) acc[m][n] = fma(q[m].x, k[n].x, acc[m][n]);
-#pragma unroll
-      for (int m = 0; m < 8; ++m)
-#pragma unroll
-        for (int n = 0; n < 8; ++n) acc[m][n] = fma(q[m].y, k[n].y, acc[m][n]);
     }
     __syncthreads();
   }
 #pragma unroll
-  for (int m = 0; m < 8; ++m)
+  for (int m = 0; m < 4; ++m)
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
-      const int i = i0 + ty + 8 * m, j = j0 + tx + 8 * n;
+      const int i = i0 + ty + 16 * m, j = j0 + tx + 8 * n;
       if (i < s.nqb && j < s.nkb) {
         const unsigned long long key = order_key(acc[m][n]);
         hi[(bh * s.nqb + i) * s.nkb + j] = (uint32_t)(key >> 32);
@@ -318,7 +315,7 @@ int vdit_attn_select_blocks(const void* q, const void* k, void* blocks, void* wo
   uint32_t* lo = hi + rows * s.nkb;
   block_means_kernel<<<dim3((unsigned)(s.nqb + s.nkb), (unsigned)chunks, (unsigned)B), 256, 0, st>>>(
       static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k), qm, km, s, flag);
-  block_scores_kernel<<<dim3((unsigned)kt, (unsigned)qt, (unsigned)bh), 64, 0, st>>>(qm, km, hi, lo, s, flag);
+  block_scores_kernel<<<dim3((unsigned)kt, (unsigned)qt, (unsigned)bh), 128, 0, st>>>(qm, km, hi, lo, s, flag);
   unsigned char* out = static_cast<unsigned char*>(blocks);
   const unsigned picks = (unsigned)((rows + 7) / 8);
   if (s.nkb <= 128) block_pick_kernel<4><<<picks, 256, 0, st>>>(hi, lo, out, rows, s, flag);
