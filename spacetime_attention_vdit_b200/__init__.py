@@ -390,6 +390,8 @@ def _launch_stream(t: torch.Tensor, name: str, stream):
         return contextlib.nullcontext(), torch.cuda.current_stream().cuda_stream
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
+    elif stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, {name} on {t.device}")
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
@@ -479,7 +481,8 @@ def attn_block_sparse_bwd(q, k, v, blocks, out, lse, d_out, scale: float = 0.0, 
                           stream=None):
     """Gradients (dq, dk, dv) of :func:`attn_block_sparse` for the gradient
     ``d_out`` of its result, from its inputs and the ``out`` and ``lse`` it
-    returned.  With every block marked: those of full or cross-attention."""
+    returned (``lse`` is needed).  With every block marked: those of full or
+    cross-attention.  dq, dk and dv may be given; they must not overlap an input."""
     _check_qk(q, k)
     bp = _check_blocks(q, k, blocks)
     B, Lq, Hh, D = q.shape
@@ -540,7 +543,8 @@ def qk_norm_rope_3d_bwd(q, k, gq, gk, grid, norm_group: int, wq=None, wk=None, e
                         theta: float = 10000.0, dq=None, dk=None, stream=None):
     """Gradients (dq, dk, dwq, dwk) of :func:`qk_norm_rope_3d`, from its inputs
     and the gradients ``gq`` and ``gk`` of its results.  dwq and dwk are float32
-    [norm_group], None where the weight was.  ``q=None`` (and ``gq=None``): K only."""
+    [norm_group], None where the weight was.  ``q=None`` (and ``gq=None``): K only.
+    dq and dk may be given; they must not overlap an input."""
     grid, split = _grid_and_split(k, grid, split)
     if (q is None) != (gq is None):
         raise ValueError("q and gq go together")

@@ -212,3 +212,14 @@ def test_tensors_of_another_device_are_refused(pretend):
         pretend.attn_select_blocks(q, k, 1)
     with pytest.raises(ValueError, match="current device"):
         pretend.rope_3d_bwd(q, q, (2, 10, 10))
+
+
+def test_a_stream_of_another_device_is_refused(pretend, monkeypatch):
+    class Stream:
+        device, cuda_stream = torch.device("cuda:1"), 0
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    q = _Pretend(1, 200, 2, 32)
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        pretend.attn_select_blocks(q, q, 1, stream=Stream())
