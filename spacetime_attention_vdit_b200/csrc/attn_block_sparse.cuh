@@ -26,7 +26,9 @@
 // marked key block, and the partial results - unnormalised O in float32, the
 // max in use and the sum of P of each row - meet in distributed shared memory:
 // each CTA joins every S-th row from its peers' copies, in the order of their
-// ranks.  No workspace, no second launch, no atomics.
+// ranks.  No workspace, no second launch, no atomics.  A sequence of one query
+// block has no second one to take turns with: there both tiles of a CTA hold the
+// same queries and share its key blocks too.
 #pragma once
 
 #include "attn_tcgen05.cuh"
@@ -230,7 +232,8 @@ __global__ void __launch_bounds__(384, 1)
   const int h = bh % p.heads;
   const int b = bh / p.heads;
   const int q0 = pair * (C::NQ * C::BM);
-  const int nq = (2 * pair + 1 < p.nqb) ? 2 : 1;   // query tiles holding rows of the sequence
+  const bool solo = kSplit && p.nqb == 1;          // both tiles hold the one query block
+  const int nq = solo || 2 * pair + 1 < p.nqb ? 2 : 1;   // query tiles holding rows of the sequence
   const int nw = (p.nkb + 31) / 32;
 
   if (threadIdx.x == 0) {
@@ -248,13 +251,14 @@ __global__ void __launch_bounds__(384, 1)
     for (int i = 0; i < nq; ++i)
 #pragma unroll
       for (int db = 0; db < C::NDB; ++db)
-        tma_load_5d(sQ + i * C::TILE_BYTES + db * C::DB_BYTES, &tmQ, q_full, db * C::DBLK, h, 0, q0 + i * C::BM, b);
+        tma_load_5d(sQ + i * C::TILE_BYTES + db * C::DB_BYTES, &tmQ, q_full, db * C::DBLK, h, 0,
+                    solo ? q0 : q0 + i * C::BM, b);
   }
   {
     const uint8_t* row = p.blocks + ((long long)bh * p.nqb + 2 * pair) * p.nkb;
     mask_words(bits, row, 1, p.nkb, warp, 12, lane);
     if (nq == 2)
-      mask_words(bits + kSparseWords, row + p.nkb, 1, p.nkb, warp, 12, lane);
+      mask_words(bits + kSparseWords, solo ? row : row + p.nkb, 1, p.nkb, warp, 12, lane);
     else
       for (int w = threadIdx.x; w < nw; w += 384) bits[kSparseWords + w] = 0u;
   }
@@ -268,22 +272,27 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t tmem = *tmem_slot;
 
   if constexpr (kSplit) {
-    // keep every splits-th block of the two rows' union (one word per thread)
+    // keep every splits-th block of the two rows' union (one word per thread), or
+    // for one query block every 2 * splits-th for each tile
     static_assert(kSparseWords <= 384, "one word per thread");
     const int w = threadIdx.x;
-    uint32_t keep = 0u, a = 0u, c = 0u;
+    uint32_t keep[2] = {0u, 0u}, a = 0u, c = 0u;
     if (w < nw) {
       int at = 0;
       for (int u = 0; u < w; ++u) at += __popc(bits[u] | bits[kSparseWords + u]);
       a = bits[w];
       c = bits[kSparseWords + w];
-      for (uint32_t left = a | c; left != 0u; left &= left - 1u, ++at)
-        if (at % p.splits == rank) keep |= left & (0u - left);
+      for (uint32_t left = a | c; left != 0u; left &= left - 1u, ++at) {
+        const uint32_t bit = left & (0u - left);
+        const int turn = at % (solo ? 2 * p.splits : p.splits);
+        if (turn == (solo ? 2 * rank : rank)) keep[0] |= bit;
+        if (turn == (solo ? 2 * rank + 1 : rank)) keep[1] |= bit;
+      }
     }
     __syncthreads();
     if (w < nw) {
-      bits[w] = a & keep;
-      bits[kSparseWords + w] = c & keep;
+      bits[w] = a & keep[0];
+      bits[kSparseWords + w] = c & keep[1];
     }
     __syncthreads();
   }
@@ -594,25 +603,26 @@ __global__ void __launch_bounds__(384, 1)
     if (warp < 8) {
       // thread = one 16-byte chunk of a row; this CTA joins rows rank, rank + splits, ...
       constexpr int CH = D / 4;
-      const int rows = min(nq * C::BM, p.Lq - q0);
+      const int rows = min(solo ? C::BM : nq * C::BM, p.Lq - q0);
       const int my_rows = rows > rank ? (rows - 1 - rank) / p.splits + 1 : 0;
+      const int tiles = solo ? 2 : 1;             // partial results of a row in each CTA
       for (int x = threadIdx.x; x < my_rows * CH; x += 256) {
         const int r = (x / CH) * p.splits + rank, ch = x % CH;
-        const float* stat = reinterpret_cast<const float*>(sQ + C::STAT_OFF) + 2 * r;
+        const float2* stat = reinterpret_cast<const float2*>(sQ + C::STAT_OFF) + r;
         const unsigned char* part = sQ + r * (D * 4) + ((ch ^ (r & 7)) << 4);
         float m = -INFINITY;
-        for (int s = 0; s < p.splits; ++s) {
-          const uint32_t at = cluster_addr(stat, s);
+        for (int s = 0; s < tiles * p.splits; ++s) {
+          const uint32_t at = cluster_addr(stat + (s % tiles) * C::BM, s / tiles);
           if (cluster_ld(at + 4) != 0.f) m = fmaxf(m, cluster_ld(at));
         }
         float l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s = 0; s < p.splits; ++s) {
-          const uint32_t at = cluster_addr(stat, s);
+        for (int s = 0; s < tiles * p.splits; ++s) {
+          const uint32_t at = cluster_addr(stat + (s % tiles) * C::BM, s / tiles);
           const float ls = cluster_ld(at + 4);
-          if (ls == 0.f) continue;                // this CTA had no key block of the row
+          if (ls == 0.f) continue;                // the tile had no key block of the row
           const float f = ex2_approx(cluster_ld(at) - m);
-          const float4 v = cluster_ld4(cluster_addr(part, s));
+          const float4 v = cluster_ld4(cluster_addr(part + (s % tiles) * C::PART_BYTES, s / tiles));
           l = fmaf(ls, f, l);
           o.x = fmaf(v.x, f, o.x);
           o.y = fmaf(v.y, f, o.y);

@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(256) block_means_kernel(const __nv_bfloat16* _
                                                           const __nv_bfloat16* __restrict__ k, double* qm, double* km,
                                                           SelectShape s, const unsigned int* flag) {
   __shared__ double part[8][32][9];
+  let_next_start();
   if (tripped(flag)) return;
   const bool is_q = (int)blockIdx.x < s.nqb;
   const int blk = is_q ? blockIdx.x : blockIdx.x - s.nqb;
@@ -138,7 +139,9 @@ __global__ void __launch_bounds__(128, 4) block_scores_kernel(const double* __re
                                                               const double* __restrict__ km, uint32_t* hi,
                                                               uint32_t* lo, SelectShape s, const unsigned int* flag) {
   __shared__ __align__(16) double st[2][2][64 * kScoreRow];
+  let_next_start();
   if (tripped(flag)) return;
+  wait_for_previous();
   const long long bh = blockIdx.z;
   const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
   const int ty = threadIdx.x >> 3, tx = threadIdx.x & 7;
@@ -205,6 +208,7 @@ __global__ void __launch_bounds__(256) block_pick_kernel(const uint32_t* __restr
                                                          const uint32_t* __restrict__ lo_words, unsigned char* blocks,
                                                          long long rows, SelectShape s, const unsigned int* flag) {
   if (tripped(flag)) return;
+  wait_for_previous();
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
@@ -315,13 +319,17 @@ int vdit_attn_select_blocks(const void* q, const void* k, void* blocks, void* wo
   uint32_t* lo = hi + rows * s.nkb;
   block_means_kernel<<<dim3((unsigned)(s.nqb + s.nkb), (unsigned)chunks, (unsigned)B), 256, 0, st>>>(
       static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k), qm, km, s, flag);
-  block_scores_kernel<<<dim3((unsigned)kt, (unsigned)qt, (unsigned)bh), 128, 0, st>>>(qm, km, hi, lo, s, flag);
+  if (cudaGetLastError() != cudaSuccess) return VDIT_ERR_CUDA;
   unsigned char* out = static_cast<unsigned char*>(blocks);
-  const unsigned picks = (unsigned)((rows + 7) / 8);
-  if (s.nkb <= 128) block_pick_kernel<4><<<picks, 256, 0, st>>>(hi, lo, out, rows, s, flag);
-  else if (s.nkb <= 256) block_pick_kernel<8><<<picks, 256, 0, st>>>(hi, lo, out, rows, s, flag);
-  else if (s.nkb <= 640) block_pick_kernel<20><<<picks, 256, 0, st>>>(hi, lo, out, rows, s, flag);
-  else block_pick_kernel<0><<<picks, 256, 0, st>>>(hi, lo, out, rows, s, flag);
+  const auto pick = s.nkb <= 128   ? block_pick_kernel<4>
+                    : s.nkb <= 256 ? block_pick_kernel<8>
+                    : s.nkb <= 640 ? block_pick_kernel<20>
+                                   : block_pick_kernel<0>;
+  if (!launch_early(block_scores_kernel, dim3((unsigned)kt, (unsigned)qt, (unsigned)bh), 128, st, qm, km, hi, lo, s, flag) ||
+      !launch_early(pick, dim3((unsigned)((rows + 7) / 8)), 256, st, hi, lo, out, rows, s, flag)) {
+    cudaGetLastError();
+    return VDIT_ERR_CUDA;
+  }
   return cudaGetLastError() == cudaSuccess ? VDIT_OK : VDIT_ERR_CUDA;
 }
 

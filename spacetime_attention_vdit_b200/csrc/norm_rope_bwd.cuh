@@ -28,6 +28,7 @@
 #pragma once
 
 #include "patchify_rope.cuh"
+#include "vdit_internal.h"
 
 namespace vdit {
 
@@ -71,6 +72,7 @@ __global__ void __launch_bounds__(norm_bwd_threads(V), 1)
   __shared__ double inv_freq[kRopeMaxPairs];
   __shared__ NormBwdGroup state[kNormBwdGroups];
   __shared__ __align__(8) uint64_t bars[kNormBwdGroups][kNormBwdMaxStages];
+  let_next_start();
   if (__syncthreads_or(watchdog_tripped())) return;     // all threads of the CTA decide alike
 
   const int tensor = s.ntens == 2 ? (int)blockIdx.y : 1;
@@ -346,6 +348,7 @@ __global__ void __launch_bounds__(1024) bwd_weights_qk_norm_rope3d_kernel(const 
                                                                           float* dwk, int group, int n_parts) {
   __shared__ float sum[32][33];
   if (watchdog_tripped()) return;
+  wait_for_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* dw = blockIdx.y ? dwk : dwq;
   if (dw == nullptr) return;

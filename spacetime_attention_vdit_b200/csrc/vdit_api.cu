@@ -920,9 +920,12 @@ int vdit_qk_norm_rope_3d_bwd(const void* q, const void* k, const void* gq, const
        : V == 3 ? launch_norm_rope_bwd<3>(wide, p, s, tab, &parts, st)
                 : launch_norm_rope_bwd<4>(wide, p, s, tab, &parts, st);
   if (rc != VDIT_OK || !weights) return rc;
-  bwd_weights_qk_norm_rope3d_kernel<<<dim3((unsigned)((norm_group + 31) / 32), 2), 1024, 0, st>>>(
-      p.parts, k_only ? nullptr : dwq, dwk, norm_group, parts);
-  return last_launch_status();
+  if (!launch_early(bwd_weights_qk_norm_rope3d_kernel, dim3((unsigned)((norm_group + 31) / 32), 2), 1024, st, p.parts,
+                    k_only ? nullptr : dwq, dwk, norm_group, parts)) {
+    cudaGetLastError();
+    return VDIT_ERR_CUDA;
+  }
+  return VDIT_OK;
 }
 
 }  // extern "C"

@@ -1,7 +1,34 @@
 // vdit_internal.h - what the library's translation units share on the host side.
 #pragma once
 
+#include <cuda_runtime.h>
+
 namespace vdit {
+
+// Launches `kernel` so that its CTAs may start while the kernel before it in the
+// stream still runs (programmatic dependent launch): it must call
+// wait_for_previous() before it touches that kernel's results, and that kernel
+// may call let_next_start().  Saves some 2 us between kernels that take little more.
+template <typename... P, typename... A>
+bool launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess;
+}
+
+#ifdef __CUDACC__
+// The kernel before this one has completed and its writes are visible.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next kernel's CTAs may take what room there is.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+#endif
 
 // Device address, on the current device, of the watchdog's flag word, or null
 // if the runtime reports an error.  The flag is one device symbol of
