@@ -377,17 +377,20 @@ def attn_cross(q, k, v, out=None, lse=None, scale: float = 0.0, stream=None):
 # Attention over selected blocks, and the gradients
 # --------------------------------------------------------------------------
 
+_NO_CONTEXT = contextlib.nullcontext()
+
+
 def _launch_stream(t: torch.Tensor, name: str, stream):
-    """(context, stream handle) for a call on ``t``'s data.  Memory that the call
+    """(context, stream handle) for a call on ``t``'s data (a CUDA tensor).  Memory that the call
     allocates (outputs, workspace) is allocated inside the context, so that it
     belongs to the stream the kernels run on: a workspace is dropped when the
     call returns, and only work queued on that stream after the kernels may get
     its memory."""
-    _dev(t, name)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    current = torch.cuda.current_device()
+    if t.device.index != current:
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{current}")
     if stream is None:
-        return contextlib.nullcontext(), torch.cuda.current_stream().cuda_stream
+        return _NO_CONTEXT, torch.cuda.current_stream(current).cuda_stream
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
     elif stream.device != t.device:
@@ -397,7 +400,7 @@ def _launch_stream(t: torch.Tensor, name: str, stream):
 
 def _same_device(device, **tensors):
     for name, t in tensors.items():
-        if isinstance(t, torch.Tensor) and t.device != device:
+        if t is not None and getattr(t, "device", device) != device:      # what is no tensor is refused by its own check
             raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
@@ -444,6 +447,8 @@ def attn_select_blocks(q, k, top_k: int, out=None, stream=None):
     [B, heads, ceil(Lq/128), ceil(Lk/128)], the ``blocks`` of
     :func:`attn_block_sparse`; masks may be combined with ``|`` and ``&``."""
     _check_qk(q, k)
+    if out is not None:
+        _check_blocks(q, k, out, "out")
     _same_device(q.device, k=k, out=out)
     ctx, st = _launch_stream(q, "q", stream)
     B, Lq, Hh, D = q.shape
@@ -451,8 +456,6 @@ def attn_select_blocks(q, k, top_k: int, out=None, stream=None):
     with ctx:
         if out is None:
             out = torch.empty((B, Hh, *_block_counts(q, k)), dtype=torch.bool, device=q.device)
-        else:
-            _check_blocks(q, k, out, "out")
         ws = _workspace(lib().vdit_attn_select_blocks_workspace(B, Lq, Lk, Hh, D), q.device)
         _check("vdit_attn_select_blocks", lib().vdit_attn_select_blocks(
             q.data_ptr(), k.data_ptr(), out.data_ptr(), ws.data_ptr(), B, Lq, Lk, Hh, D, int(top_k), st))
