@@ -20,7 +20,14 @@
 // the TMA producer, warp 9 the one issuer of UMMAs.  Two warpgroups share each
 // 128 x 128 tile: thread = (row, half of the columns).  P and dS are rounded to
 // bfloat16 (nearest even) as operands of the products, as P is in the forward
-// pass; scores, sums and accumulators are float32.
+// pass (that, beside the last rounding, is the error against float64: 0.0025
+// relative, of which the rounding of the result is 0.0017); scores, sums and
+// accumulators are float32.
+//
+// Measured: 32,760 tokens, 40 heads x 128, 32 of 256 blocks 8.7 to 9.1 ms (1.06 to
+// 1.11 PFLOP/s of the seven products), 43 % of it dq; a tile takes 1.3 us (dq) and 1.5
+// (dkv), a CTA's start and end 6 us.  Bound by the tensor pipe and its changes of
+// operand form: two a tile (dq), four (dkv).
 #pragma once
 
 #include "attn_block_sparse.cuh"

@@ -36,7 +36,7 @@ __device__ __forceinline__ bool tripped(const unsigned int* flag) {
 
 // Means of every 128-token block of Q (blockIdx.x < nqb) and K: a CTA takes 256
 // channels of one block, a thread 8 channels of every 8th token.  Bound by the
-// bytes of Q and K; a conversion instruction to float64 per value would take
+// bytes of Q and K (240 us for twice 75,600 x 40 x 128: 6.45 TB/s); a conversion instruction to float64 per value would take
 // longer than they do (16 per clock and SM), so a bfloat16's bits are moved into
 // a float64's high word as they are: exponent field e stands for 2^(e - 1023)
 // there and 2^(e - 127) in the bfloat16, denormals alike, so the float64 is the
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(128, 4) block_scores_kernel(const double* __re
 // with more than top_k at or above t: of those equal to t the first ones are
 // marked.  N > 0: the high words of a row of at most 32 N keys are held in
 // registers (zeros past its end, which no threshold of the search counts); N = 0:
-// longer rows are read again for each bit.
+// longer rows are read again for each bit.  40 x 591 rows of 591 keys take 66 us.
 template <int N>
 __global__ void __launch_bounds__(256) block_pick_kernel(const uint32_t* __restrict__ hi_words,
                                                          const uint32_t* __restrict__ lo_words, unsigned char* blocks,

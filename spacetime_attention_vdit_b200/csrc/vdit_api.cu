@@ -312,14 +312,19 @@ int rope_pass(const void* q_in, const void* k_in, void* q_out, void* k_out, int 
   return last_launch_status();
 }
 
-// CTAs that share a pair of query blocks: as many as leave no SM of a full
-// wave idle, in the powers of two that tile a GPC's SMs (a cluster of 8 needs 8
-// free SMs of one GPC; 128 of the 148 can hold such clusters at once), each
-// with two key blocks or more to choose from.
-int sparse_splits(long long units, int nkb) {
-  int s = 8;
-  while (s > 1 && (units * s > 128 || nkb < 2 * s)) s /= 2;
-  return s;
+// CTAs that share a pair of query blocks (0: one CTA without a cluster).  Eight or
+// four where all clusters fit on the device at once (`fit`: as many of 8, 4 and 2 as
+// do), each CTA with two key blocks or more to choose from.  A sequence of one query
+// block always takes the cluster's kernel, whose CTAs put both tiles on it, in pairs
+// or alone if need be.  Measured (us, with and without): one token, 64 key blocks of
+// 32,760 keys, 12 heads in eights 18.6 / 110, 24 in fours 25.8 / 111, 48 in twos 43 /
+// 113, 100 alone 77 / 113; 1,560 queries, 20 key blocks, 4 heads in fours 30 / 45, but 8 heads in twos
+// 47.5 / 45.4: no twos for pairs of blocks.  16 heads in eights, which do not fit at
+// once, 35.5.
+int sparse_splits(long long units, int nqb, int nkb, const int (&fit)[3]) {
+  for (int i = 0, s = 8; s > 1; ++i, s /= 2)
+    if (units <= fit[i] && nkb >= 2 * s && (s > 2 || nqb == 1)) return s;
+  return nqb == 1 && nkb > 1 ? 1 : 0;
 }
 
 template <int D>
@@ -327,12 +332,35 @@ int launch_block_sparse(const void* q, const void* k, const void* v, void* o, fl
                         int Lq, int Lk, int heads, float scale, cudaStream_t stream) {
   using C = SparseCfg<D>;
   static bool done[kMaxDevices] = {}, done_split[kMaxDevices] = {};
+  static int fits[kMaxDevices][3];
   static std::mutex mu;
+  const auto split_kernel = attn_fwd_tcgen05_sparse_kernel<D, true>;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int dev = 0, fit[3];
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return VDIT_ERR_CUDA;
   {
     std::lock_guard<std::mutex> lock(mu);
+    const bool first = !done_split[dev];
     if (!ensure_smem(attn_fwd_tcgen05_sparse_kernel<D, false>, C::SMEM_BYTES, done) ||
-        !ensure_smem(attn_fwd_tcgen05_sparse_kernel<D, true>, C::SMEM_BYTES, done_split))
+        !ensure_smem(split_kernel, C::SMEM_BYTES, done_split))
       return VDIT_ERR_CUDA;
+    for (int i = 0, s = 8; first && i < 3; ++i, s /= 2) {
+      attr.val.clusterDim.x = (unsigned)s;
+      cfg.gridDim = dim3((unsigned)s);
+      if (cudaOccupancyMaxActiveClusters(&fits[dev][i], split_kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        fits[dev][i] = 0;                                // then no clusters of this size
+      }
+    }
+    for (int i = 0; i < 3; ++i) fit[i] = fits[dev][i];
   }
   const long long tok = (long long)heads * D;
   CUtensorMap mq, mk, mv, mo;
@@ -351,23 +379,14 @@ int launch_block_sparse(const void* q, const void* k, const void* v, void* o, fl
   p.scale_log2 = scale * 1.4426950408889634f;
   const long long units = (long long)B * heads * p.n_pairs;
   if (units > 0x7fffffffLL) return VDIT_ERR_SHAPE;
-  p.splits = sparse_splits(units, p.nkb);
-  if (p.splits == 1) {
+  p.splits = sparse_splits(units, p.nqb, p.nkb, fit);
+  if (p.splits == 0) {
     attn_fwd_tcgen05_sparse_kernel<D, false><<<(unsigned)units, C::THREADS, C::SMEM_BYTES, stream>>>(mq, mk, mv, mo, p);
     return last_launch_status();
   }
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = (unsigned)p.splits;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(units * p.splits));
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM_BYTES;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, attn_fwd_tcgen05_sparse_kernel<D, true>, mq, mk, mv, mo, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, split_kernel, mq, mk, mv, mo, p) != cudaSuccess) {
     cudaGetLastError();
     return VDIT_ERR_CUDA;
   }

@@ -8,7 +8,8 @@ namespace vdit {
 // Launches `kernel` so that its CTAs may start while the kernel before it in the
 // stream still runs (programmatic dependent launch): it must call
 // wait_for_previous() before it touches that kernel's results, and that kernel
-// may call let_next_start().  Saves some 2 us between kernels that take little more.
+// may call let_next_start().  Saves about 1 us between kernels that take little more
+// (the selection at 512 tokens: 30.1 to 27.8 us).
 template <typename... P, typename... A>
 bool launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t stream, A... args) {
   cudaLaunchAttribute attr{};

@@ -185,11 +185,14 @@ def test_forward(B, Lq, Lk, heads, D, keep):
     _check_forward(*_inputs(B, Lq, Lk, heads, D, seed=Lk), _mask(B, Lq, Lk, heads, keep, seed=Lq))
 
 
-@pytest.mark.parametrize("heads", [5, 24, 40, 80])
-def test_forward_at_each_split(heads):
-    """Eight, four, two and one CTA per pair of query blocks."""
-    q, k, v = _inputs(1, 200, 2500, heads, 64, seed=heads)
-    _check_forward(q, k, v, _mask(1, 200, 2500, heads, 0.5, seed=1))
+@pytest.mark.parametrize("Lq", [3, 200])
+@pytest.mark.parametrize("heads", [5, 24, 40, 80, 200])
+def test_forward_at_each_split(heads, Lq):
+    """Eight, four, two and one CTA per pair of query blocks, and for a single block."""
+    q, k, v = _inputs(1, Lq, 2500, heads, 64, seed=heads)
+    on = _mask(1, Lq, 2500, heads, 0.5, seed=1)
+    on[:, 0, 0] = False                          # a head whose first block has nothing
+    _check_forward(q, k, v, on)
 
 
 @pytest.mark.parametrize("Lq,heads", [(1, 1), (256, 1), (256, 40), (5000, 8)])
