@@ -102,10 +102,11 @@ __device__ __forceinline__ void mask_words(uint32_t* words, const uint8_t* row, 
 // ---- UMMAs from precomputed descriptors
 //
 // One thread issues every UMMA, and at 16 per tile step what it computes for each
-// weighs: building both 64-bit descriptors from addresses every time took longer
-// than the tensor core needs for the products.  The words of a descriptor are
-// built once per operand; a UMMA's own is an addition to the address field of the
-// low word (14 bits of 16 bytes: shared memory never carries out of it).
+// weighs.  So the words of a descriptor are built once per operand, and a UMMA's own
+// is an addition to the address field of the low word (14 bits of 16 bytes: shared
+// memory never carries out of it): 75,600 tokens x 40 heads 15.7 -> 14.7 ms; with the
+// tile known at compile time and ring positions stepped instead of divided, 15.4 ->
+// 14.3 (another box).
 
 struct UmmaDesc {
   uint32_t lo, hi;
