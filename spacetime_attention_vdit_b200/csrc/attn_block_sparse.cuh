@@ -30,7 +30,7 @@
 // block has no second one to take turns with: there both tiles of a CTA hold the
 // same queries and share its key blocks too.
 //
-// Measured: 75,600 tokens, 40 heads x 128, 74 of 591 blocks 14.6 to 14.8 ms (1.0
+// Measured: 75,600 tokens, 40 heads x 128, 74 of 591 blocks 14.3 to 14.8 ms (1.0
 // PFLOP/s; the dense kernel with as many keys 13.5 ms); one token over 32,760 keys, 12
 // heads, 64 blocks 18 us.  Bound as the dense kernel is, by the tensor pipe's changes
 // of operand form and the exponentials; a CTA's start (mask, first copies) and end

@@ -21,8 +21,8 @@
 // then.  The CTA's part of dw goes to the workspace and a second kernel adds the
 // CTAs' parts in a fixed order (no atomics: the same result on every run).
 //
-// Measured: 75,600 tokens x 5,120 channels, one group per token, Q and K: 926 to 972
-// us (4.8 to 5.0 TB/s, 0.73 to 0.77 of the copy rate); 7,800 x 12 x 128 per head: 41 us.
+// Measured: 75,600 tokens x 5,120 channels, one group per token, Q and K: 912 to 972
+// us (4.8 to 5.1 TB/s, 0.73 to 0.78 of the copy rate); 7,800 x 12 x 128 per head: 41 us.
 // Bound by HBM in the end, but what had to be pared down is instructions: a
 // vector takes some 100 (half of them the formula's multiply-adds), and a warp
 // some 150 more per token for the sums, the barrier and the loop, which is why a
