@@ -392,7 +392,9 @@ def _launch_stream(t: torch.Tensor, name: str, stream):
     if stream is None:
         return _NO_CONTEXT, torch.cuda.current_stream(current).cuda_stream
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
+        # 0 is the default stream's handle; an ExternalStream of 0 would be a new stream
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream(current)
     elif stream.device != t.device:
         raise ValueError(f"stream is on {stream.device}, {name} on {t.device}")
     return torch.cuda.stream(stream), stream.cuda_stream
