@@ -451,8 +451,9 @@ int vdit_rope_3d_bwd(const void* gq, const void* gk, void* dq, void* dk,
  * wanted); with both NULL workspace may be NULL, else it has
  * vdit_qk_norm_rope_3d_bwd_workspace bytes, 16-byte aligned, used by this call
  * alone until the stream has run it.  q, gq and dq all NULL: K alone (dwq is then
- * not written).  dq and dk must not overlap any input.  float32 throughout, dq
- * and dk rounded once to bfloat16; the sums of dwq and dwk are taken in a fixed
+ * not written).  dq and dk must not overlap any input.  float32 throughout (with
+ * eps 0 or next to it: for groups whose root mean square is between 1e-18 and
+ * 1e17), dq and dk rounded once to bfloat16; the sums of dwq and dwk are taken in a fixed
  * order, so they do not change from run to run.
  * Errors as for vdit_qk_norm_rope_3d.
  * Watchdog: device-wide (see the conventions above).
