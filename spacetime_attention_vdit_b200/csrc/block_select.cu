@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(128, 4) block_scores_kernel(const double* __re
                                                               uint32_t* lo, SelectShape s, const unsigned int* flag) {
   __shared__ __align__(16) double st[2][2][64 * kScoreRow];
   let_next_start();
-  if (tripped(flag)) return;
   wait_for_previous();
+  if (tripped(flag)) return;
   const long long bh = blockIdx.z;
   const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
   const int ty = threadIdx.x >> 3, tx = threadIdx.x & 7;
@@ -207,8 +207,8 @@ template <int N>
 __global__ void __launch_bounds__(256) block_pick_kernel(const uint32_t* __restrict__ hi_words,
                                                          const uint32_t* __restrict__ lo_words, unsigned char* blocks,
                                                          long long rows, SelectShape s, const unsigned int* flag) {
-  if (tripped(flag)) return;
   wait_for_previous();
+  if (tripped(flag)) return;
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;

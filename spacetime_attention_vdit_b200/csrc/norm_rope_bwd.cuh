@@ -353,8 +353,8 @@ __global__ void __launch_bounds__(norm_bwd_threads(V), 1)
 __global__ void __launch_bounds__(1024) bwd_weights_qk_norm_rope3d_kernel(const float* __restrict__ parts, float* dwq,
                                                                           float* dwk, int group, int n_parts) {
   __shared__ float sum[32][33];
-  if (watchdog_tripped()) return;
   wait_for_previous();
+  if (watchdog_tripped()) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* dw = blockIdx.y ? dwk : dwq;
   if (dw == nullptr) return;

@@ -6,10 +6,13 @@
 namespace vdit {
 
 // Launches `kernel` so that its CTAs may start while the kernel before it in the
-// stream still runs (programmatic dependent launch): it must call
-// wait_for_previous() before it touches that kernel's results, and that kernel
-// may call let_next_start().  Saves about 1 us between kernels that take little more
-// (the selection at 512 tokens: 30.1 to 27.8 us).
+// stream still runs (programmatic dependent launch), once that kernel has called
+// let_next_start().  Saves about 1 us between kernels that take little more (the
+// selection at 512 tokens: 30.1 to 27.8 us).  Every thread of `kernel` must call
+// wait_for_previous() before it reads anything or returns, also where it has nothing
+// to do: the kernel after it waits for it alone, and would else start while the one
+// before still writes to memory that the caller has back by then.  The watchdog's
+// flag is read after that wait too, so that the previous kernel's waits are in it.
 template <typename... P, typename... A>
 bool launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t stream, A... args) {
   cudaLaunchAttribute attr{};

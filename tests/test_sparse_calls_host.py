@@ -2,6 +2,8 @@
 device (no GPU needed): the stream they launch on, what they refuse, and what
 their kernels may not do."""
 import contextlib
+import os
+import re
 
 import pytest
 import torch
@@ -29,3 +31,58 @@ def test_a_stream_handle_launches_on_that_stream(monkeypatch, handle, want):
     assert got == want
     with context as st:
         assert st.cuda_stream == want            # what the call allocates belongs to the same stream
+
+
+def _sources():
+    from spacetime_attention_vdit_b200 import build
+    return {name: re.sub(r"//[^\n]*", "", open(os.path.join(build.CSRC, name)).read())
+            for name in sorted(os.listdir(build.CSRC)) if name.endswith((".cu", ".cuh", ".h"))}
+
+
+def _kernels():
+    """{name: (parameter list, body)} of every kernel in the sources, comments gone."""
+    out = {}
+    for text in _sources().values():
+        for m in re.finditer(r"__global__ void\s+(?:__launch_bounds__\([^{;]*?\)\s+)?(\w+)\s*\(", text):
+            at, depth = m.end(), 1
+            while depth:
+                depth += {"(": 1, ")": -1}.get(text[at], 0)
+                at += 1
+            params, begin = text[m.end():at - 1], text.index("{", at)
+            end, depth = begin + 1, 1
+            while depth:
+                depth += {"{": 1, "}": -1}.get(text[end], 0)
+                end += 1
+            out[m.group(1)] = (params, text[begin + 1:end - 1])
+    return out
+
+
+def _launched_early():
+    """Names of the kernels that launch_early() starts, through a variable too."""
+    names, kernels = set(), _kernels()
+    for text in _sources().values():
+        for m in re.finditer(r"launch_early\((\w+),", text):
+            name = m.group(1)
+            if name in kernels:
+                names.add(name)
+                continue
+            held = re.search(rf"auto {name} =([^;]*);", text)
+            assert held, name
+            picked = set(re.findall(r"\b(\w+_kernel)\b", held.group(1)))
+            assert picked and picked <= set(kernels)
+            names |= picked
+    return names
+
+
+def test_kernels_launched_early_wait_before_they_read_or_leave():
+    """A kernel that may start before its predecessor has finished waits for it
+    first: before any return (the next kernel of the stream waits for this one
+    alone) and before it reads the watchdog's flag or memory."""
+    kernels, early = _kernels(), _launched_early()
+    assert {"block_scores_kernel", "block_pick_kernel", "bwd_weights_qk_norm_rope3d_kernel"} <= early
+    for name in early:
+        before, found, _ = kernels[name][1].partition("wait_for_previous();")
+        assert found, name
+        for statement in before.split(";"):
+            words = statement.split()
+            assert not words or words[0] in ("__shared__", "let_next_start()"), (name, statement)
