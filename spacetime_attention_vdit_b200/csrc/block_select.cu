@@ -135,8 +135,7 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 
-__global__ void __launch_bounds__(128, 4) block_scores_kernel(const double* __restrict__ qm,
-                                                              const double* __restrict__ km, uint32_t* hi,
+__global__ void __launch_bounds__(128, 4) block_scores_kernel(const double* qm, const double* km, uint32_t* hi,
                                                               uint32_t* lo, SelectShape s, const unsigned int* flag) {
   __shared__ __align__(16) double st[2][2][64 * kScoreRow];
   let_next_start();
@@ -204,9 +203,9 @@ __global__ void __launch_bounds__(128, 4) block_scores_kernel(const double* __re
 // registers (zeros past its end, which no threshold of the search counts); N = 0:
 // longer rows are read again for each bit.  40 x 591 rows of 591 keys take 66 us.
 template <int N>
-__global__ void __launch_bounds__(256) block_pick_kernel(const uint32_t* __restrict__ hi_words,
-                                                         const uint32_t* __restrict__ lo_words, unsigned char* blocks,
-                                                         long long rows, SelectShape s, const unsigned int* flag) {
+__global__ void __launch_bounds__(256) block_pick_kernel(const uint32_t* hi_words, const uint32_t* lo_words,
+                                                         unsigned char* blocks, long long rows, SelectShape s,
+                                                         const unsigned int* flag) {
   wait_for_previous();
   if (tripped(flag)) return;
   const int lane = threadIdx.x & 31;

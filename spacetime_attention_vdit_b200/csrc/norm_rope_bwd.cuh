@@ -350,8 +350,8 @@ __global__ void __launch_bounds__(norm_bwd_threads(V), 1)
 // dw[c] = the CTAs' parts of channel c, added in a fixed order: a CTA takes 32
 // channels of one tensor, its 32 warps the CTAs w, w + 32, ... (at most five loads
 // each, all in flight at once).
-__global__ void __launch_bounds__(1024) bwd_weights_qk_norm_rope3d_kernel(const float* __restrict__ parts, float* dwq,
-                                                                          float* dwk, int group, int n_parts) {
+__global__ void __launch_bounds__(1024) bwd_weights_qk_norm_rope3d_kernel(const float* parts, float* dwq, float* dwk,
+                                                                          int group, int n_parts) {
   __shared__ float sum[32][33];
   wait_for_previous();
   if (watchdog_tripped()) return;
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(1024) bwd_weights_qk_norm_rope3d_kernel(const 
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int row = warp + 32 * i;
-    v[i] = c < group && row < n_parts ? __ldg(from + (long long)row * group + c) : 0.f;
+    v[i] = c < group && row < n_parts ? __ldcg(from + (long long)row * group + c) : 0.f;
   }
   float a = v[0];
 #pragma unroll

@@ -13,6 +13,10 @@ namespace vdit {
 // to do: the kernel after it waits for it alone, and would else start while the one
 // before still writes to memory that the caller has back by then.  The watchdog's
 // flag is read after that wait too, so that the previous kernel's waits are in it.
+// What the kernel before writes is not read-only for the lifetime of `kernel`: it is
+// read by plain loads or __ldcg, never by __ldg or through a __restrict__ pointer
+// (the compiler may take the non-coherent path there, and move the load ahead of
+// the wait).
 template <typename... P, typename... A>
 bool launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t stream, A... args) {
   cudaLaunchAttribute attr{};

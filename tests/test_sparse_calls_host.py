@@ -86,3 +86,14 @@ def test_kernels_launched_early_wait_before_they_read_or_leave():
         for statement in before.split(";"):
             words = statement.split()
             assert not words or words[0] in ("__shared__", "let_next_start()"), (name, statement)
+
+
+def test_kernels_launched_early_read_coherently():
+    """Memory that the previous kernel may still be writing when this one starts is
+    not read-only for its lifetime: no non-coherent loads, and no __restrict__ that
+    would let the compiler use them."""
+    kernels = _kernels()
+    for name in _launched_early():
+        params, body = kernels[name]
+        assert "__restrict__" not in params, name
+        assert "__ldg" not in body and "ld.global.nc" not in body and "__restrict__" not in body, name
