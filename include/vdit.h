@@ -447,8 +447,8 @@ int vdit_rope_3d_bwd(const void* gq, const void* gk, void* dq, void* dk,
  *   dx = r * (u w) - x * r^3 * mean(x u w)        dw = sum of u x r
  * (dw over all tokens and, with a per-head group, over the heads).
  * q, k: the forward call's inputs; gq, gk: the gradients of its outputs; wq, wk
- * as there (NULL: weight 1).  dwq, dwk: float32 [norm_group] or NULL (not
- * wanted); with both NULL workspace may be NULL, else it has
+ * as there (NULL: weight 1).  dwq, dwk: float32 [norm_group], 4-byte aligned, or
+ * NULL (not wanted); with both NULL workspace may be NULL, else it has
  * vdit_qk_norm_rope_3d_bwd_workspace bytes, 16-byte aligned, used by this call
  * alone until the stream has run it.  q, gq and dq all NULL: K alone (dwq is then
  * not written).  dq and dk must not overlap any input.  float32 throughout (with

@@ -902,6 +902,8 @@ int vdit_qk_norm_rope_3d_bwd(const void* q, const void* k, const void* gq, const
   const void* ptrs[] = {q, k, gq, gk, dq, dk, wq, wk, workspace};
   for (const void* x : ptrs)
     if (x && !aligned16(x)) return VDIT_ERR_ALIGN;
+  for (const float* x : {dwq, dwk})
+    if ((reinterpret_cast<uintptr_t>(x) & 3u) != 0) return VDIT_ERR_ALIGN;
   const long long tab = rope_table_entries(Tg, Hg, Wg, d_t, d_h, d_w);
   if (tab > kNormMaxTable) return VDIT_ERR_UNSUPPORTED;
   RopeShape s;

@@ -8,8 +8,8 @@ import re
 import pytest
 import torch
 
-from tests.test_abi_host import L  # noqa: F401  (fixture)
-from tests.test_sparse_host import _Pretend
+from tests.test_abi_host import ALIGN, FAKE, L  # noqa: F401  (L: fixture)
+from tests.test_sparse_host import _Pretend, norm_bwd
 
 
 @pytest.mark.parametrize("handle,want", [(0, 0), (1, 1), (0x7f00, 0x7f00)])
@@ -97,3 +97,10 @@ def test_kernels_launched_early_read_coherently():
         params, body = kernels[name]
         assert "__restrict__" not in params, name
         assert "__ldg" not in body and "ld.global.nc" not in body and "__restrict__" not in body, name
+
+
+def test_weight_gradients_are_checked_for_alignment(L):  # noqa: F811
+    """dwq and dwk are written as float32: an address between two of them is refused."""
+    for name in ("dwq", "dwk"):
+        assert norm_bwd(L, **{name: FAKE + 2}) == ALIGN
+        assert norm_bwd(L, **{name: FAKE + 1}) == ALIGN
