@@ -44,7 +44,7 @@ struct SparseBwdParams {
 };
 
 enum : int {
-  kSiteBwdIn = 40, kSiteBwdRow, kSiteBwdCol, kSiteBwdRowFree, kSiteBwdColFree, kSiteBwdS, kSiteBwdDp, kSiteBwdP,
+  kSiteBwdIn = 48, kSiteBwdRow, kSiteBwdCol, kSiteBwdRowFree, kSiteBwdColFree, kSiteBwdS, kSiteBwdDp, kSiteBwdP,
   kSiteBwdDs, kSiteBwdStat, kSiteBwdStatFree, kSiteBwdDone
 };
 

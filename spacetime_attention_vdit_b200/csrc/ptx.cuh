@@ -19,6 +19,9 @@ namespace vdit {
 // ---------------------------------------------------------------------------
 
 // Bit 0: some wait ran out.  Bits 8..15: the site of the first one seen.
+// Sites: 1..10 full, cross, space and block-sparse attention (one set of roles), 20..22
+// the short time pass, 30, 31 norm + rotation, 32, 33 its gradient, 40..43 the patch
+// embedding, 48..59 the gradients of block-sparse attention.
 __device__ unsigned int g_watchdog;
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s per wait

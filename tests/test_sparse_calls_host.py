@@ -104,3 +104,25 @@ def test_weight_gradients_are_checked_for_alignment(L):  # noqa: F811
     for name in ("dwq", "dwk"):
         assert norm_bwd(L, **{name: FAKE + 2}) == ALIGN
         assert norm_bwd(L, **{name: FAKE + 1}) == ALIGN
+
+
+def test_watchdog_sites_are_told_apart():
+    """A timeout reports the number of its wait alone: no two waits of different
+    kernels may have one number, and it has to fit its 8 bits."""
+    sites, literal = {}, set()
+    for name, text in _sources().items():
+        for body in re.findall(r"enum : int \{([^}]*)\}", text) + re.findall(r"constexpr int (kSite[^;]*);", text):
+            if "kSite" not in body:
+                continue
+            value = -1
+            for item in body.split(","):
+                key, _, given = (x.strip() for x in item.partition("="))
+                value = int(given) if given else value + 1
+                assert key not in sites, key
+                sites[key] = value
+        literal |= {int(x) for x in re.findall(r"(?:mbar_wait|warp_wait|mbar_drain_site)\([^;]*?, (\d+)\)\)", text)}
+        literal |= {int(x) for x in re.findall(r"watchdog_trip\((\d+)\)", text)}
+    assert len(sites) > 20 and literal
+    values = list(sites.values()) + sorted(literal)
+    assert len(set(values)) == len(values), sorted((v, k) for k, v in sites.items() if values.count(v) > 1)
+    assert all(0 < v < 256 for v in values)
