@@ -362,18 +362,30 @@ constexpr int kNormVecs = 8;        // vectors per thread: heads * head_dim <= 1
 constexpr int kSiteNormFull = 30, kSiteNormDrain = 31;   // watchdog wait sites
 constexpr int kNormMaxTable = 8192;  // (cos, sin) table entries: Tg*d_t/2 + Hg*d_h/2 + Wg*d_w/2
 
+// The CTA's small variables, at the head of its dynamic shared memory: as static ones
+// they would be padded to the alignment of the dynamic part, and at width 5,120 with
+// 3,841 to 3,952 table entries (56 to 60 latent frames of 1280x720) the KB costs the
+// SM's second CTA (20.3 against 13.8 ns a token).
+struct NormHead {
+  float wsum[2][4];                                     // [tensor][warp]: sums of squares
+  float2 cs[2][kRopeMaxPairs];                          // the token's pairs, by token parity
+  uint64_t full[kNormStages];
+};
+constexpr int kNormHeadBytes = (sizeof(NormHead) + 127) / 128 * 128;
+
 template <bool kWide>   // the group is the token's whole heads*D vector
 __global__ void __launch_bounds__(kNormThreads) qk_norm_rope3d_kernel(
     const __nv_bfloat16* q_in, const __nv_bfloat16* k_in, __nv_bfloat16* q_out, __nv_bfloat16* k_out,
     const float* __restrict__ wq, const float* __restrict__ wk, RopeShape s, int group, float eps, double theta) {
-  __shared__ float wsum[2][4];                          // [tensor][warp]: sums of squares
-  __shared__ float2 cs[2][kRopeMaxPairs];              // the token's pairs, by token parity
-  __shared__ __align__(8) uint64_t full[kNormStages];
+  NormHead& head = *reinterpret_cast<NormHead*>(dyn_smem);
+  auto& wsum = head.wsum;
+  auto& cs = head.cs;
+  auto& full = head.full;
   if (__syncthreads_or(watchdog_tripped())) return;    // all threads of the CTA decide alike
 
   const int vec_per_head = s.D / 8;
   const int nv = s.heads * vec_per_head;                // vectors per token and tensor
-  uint4* ring = reinterpret_cast<uint4*>(dyn_smem);    // [stage][Q row, K row] of nv vectors each
+  uint4* ring = reinterpret_cast<uint4*>(dyn_smem + kNormHeadBytes);   // [stage][Q row, K row] of nv vectors each
   // per-axis tables: time [Tg][d_t/2], then height [Hg][d_h/2], then width [Wg][d_w/2]
   float2* tab = reinterpret_cast<float2*>(ring + (size_t)kNormStages * 2 * nv);
   const int pt = s.d_t / 2, ph = s.d_h / 2, pw = s.d_w / 2;

@@ -707,13 +707,14 @@ int vdit_qk_norm_rope_3d(const void* q_in, const void* k_in, void* q_out, void* 
   // the ring (Q and K rows of kNormStages tokens) and the per-axis (cos, sin) tables
   const long long tab = (long long)Tg * (d_t / 2) + (long long)Hg * (d_h / 2) + (long long)Wg * (d_w / 2);
   if (tab > kNormMaxTable) return VDIT_ERR_UNSUPPORTED;
-  const int smem = kNormStages * 2 * (int)width * 2 + (int)tab * 8;
+  const int smem = kNormHeadBytes + kNormStages * 2 * (int)width * 2 + (int)tab * 8;
   {
     static bool done_n[kMaxDevices] = {}, done_w[kMaxDevices] = {};
     static std::mutex mu;
     std::lock_guard<std::mutex> lock(mu);
-    if (!ensure_smem(qk_norm_rope3d_kernel<false>, kNormStages * 2 * 8192 * 2 + kNormMaxTable * 8, done_n) ||
-        !ensure_smem(qk_norm_rope3d_kernel<true>, kNormStages * 2 * 8192 * 2 + kNormMaxTable * 8, done_w))
+    constexpr int most = kNormHeadBytes + kNormStages * 2 * 8192 * 2 + kNormMaxTable * 8;
+    if (!ensure_smem(qk_norm_rope3d_kernel<false>, most, done_n) ||
+        !ensure_smem(qk_norm_rope3d_kernel<true>, most, done_w))
       return VDIT_ERR_CUDA;
   }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
