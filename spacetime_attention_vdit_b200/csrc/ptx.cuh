@@ -61,6 +61,16 @@ __device__ __forceinline__ unsigned char* smem_base_1024() {
   return dyn_smem + ((1024u - (smem_u32(dyn_smem) & 1023u)) & 1023u);
 }
 
+// The same address, from an array declared with less alignment (all dynamic arrays
+// start at one address).  The compiler then does not see that the rounding changes
+// nothing, and keeps the base in a register where it would else put a constant into
+// every address; some kernels are faster so.
+extern __shared__ __align__(128) unsigned char dyn_smem_128[];
+
+__device__ __forceinline__ unsigned char* smem_base_1024_in_register() {
+  return dyn_smem_128 + ((1024u - (smem_u32(dyn_smem_128) & 1023u)) & 1023u);
+}
+
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
 }
