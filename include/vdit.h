@@ -358,8 +358,9 @@ int vdit_attn_cross(const void* q, const void* k, const void* v, void* o, float*
  * written; workspace: vdit_attn_select_blocks_workspace bytes, 16-byte aligned,
  * used by this call alone until the stream has run it.
  * Errors: VDIT_ERR_NULL, VDIT_ERR_SHAPE (also: top_k below 1 or above
- * ceil(Lk/128)), VDIT_ERR_ALIGN, VDIT_ERR_UNSUPPORTED (head_dim; more than
- * 6,144 key blocks), VDIT_ERR_CUDA.
+ * ceil(Lk/128); B * heads above 65,535 - split the batch, whose rows are
+ * independent; Lq above 536,862,720), VDIT_ERR_ALIGN, VDIT_ERR_UNSUPPORTED
+ * (head_dim; more than 6,144 key blocks), VDIT_ERR_CUDA.
  * Watchdog: device-wide (see the conventions above).
  */
 int vdit_attn_select_blocks(const void* q, const void* k, void* blocks, void* workspace,

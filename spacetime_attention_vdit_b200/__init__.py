@@ -447,7 +447,8 @@ def attn_select_blocks(q, k, top_k: int, out=None, stream=None):
     highest product of their mean key with its mean query (ties: the lower
     block).  q [B, Lq, heads, D], k [B, Lk, heads, D] bfloat16 -> truth values
     [B, heads, ceil(Lq/128), ceil(Lk/128)], the ``blocks`` of
-    :func:`attn_block_sparse`; masks may be combined with ``|`` and ``&``."""
+    :func:`attn_block_sparse`; masks may be combined with ``|`` and ``&``.  At most
+    65,535 heads in all, B * heads (more: in parts of the batch)."""
     _check_qk(q, k)
     if out is not None:
         _check_blocks(q, k, out, "out")

@@ -8,8 +8,8 @@ import re
 import pytest
 import torch
 
-from tests.test_abi_host import ALIGN, FAKE, L  # noqa: F401  (L: fixture)
-from tests.test_sparse_host import _Pretend, norm_bwd
+from tests.test_abi_host import ALIGN, FAKE, L, SHAPE  # noqa: F401  (L: fixture)
+from tests.test_sparse_host import _Pretend, norm_bwd, select
 
 
 @pytest.mark.parametrize("handle,want", [(0, 0), (1, 1), (0x7f00, 0x7f00)])
@@ -126,3 +126,15 @@ def test_watchdog_sites_are_told_apart():
     values = list(sites.values()) + sorted(literal)
     assert len(set(values)) == len(values), sorted((v, k) for k, v in sites.items() if values.count(v) > 1)
     assert all(0 < v < 256 for v in values)
+
+
+def test_the_selections_limits_are_the_headers(L):  # noqa: F811
+    """Sizes past the launch grid are refused as the header says, before any launch."""
+    from tests.conftest import ROOT
+    assert select(L, B=1, heads=65536, Lq=1, Lk=1, D=32, top_k=1) == SHAPE
+    assert select(L, B=65536, heads=1, Lq=1, Lk=1, D=32, top_k=1) == SHAPE
+    assert select(L, B=256, heads=256, Lq=1, Lk=1, D=32, top_k=1) == SHAPE
+    assert select(L, heads=1, Lq=536_862_721, D=32) == SHAPE
+    header = re.sub(r"\s*\n \* ?", " ", open(os.path.join(ROOT, "include", "vdit.h")).read())
+    text = header[header.index("vdit_attn_select_blocks - "):header.index("int vdit_attn_select_blocks(")]
+    assert "B * heads above 65,535" in text and "Lq above 536,862,720" in text
