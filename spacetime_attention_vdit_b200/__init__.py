@@ -27,6 +27,8 @@ Calls (see ``include/vdit.h`` for the exact definitions and sources):
 and the gradients of the attention sub-layer's steps:
 
 * :func:`attn_block_sparse_bwd`, :func:`rope_3d_bwd`, :func:`qk_norm_rope_3d_bwd`
+
+(to be chained by hand: no call records anything for autograd).
 """
 from __future__ import annotations
 

@@ -32,9 +32,10 @@
 //
 // Measured: 75,600 tokens, 40 heads x 128, 74 of 591 blocks 14.3 to 14.8 ms (1.0
 // PFLOP/s; the dense kernel with as many keys 13.5 ms); one token over 32,760 keys, 12
-// heads, 64 blocks 18 us.  Bound as the dense kernel is, by the tensor pipe's changes
-// of operand form and the exponentials; a CTA's start (mask, first copies) and end
-// take 7 us of its 28 at 11 blocks.
+// heads, 64 blocks 18 us in a graph (22 by a call: the host's work is longer).  Bound as
+// the dense kernel is, by the tensor pipe's changes of operand form and the
+// exponentials; a CTA's start (mask, first copies) and end take 7 us of its 28 at 11
+// blocks.
 #pragma once
 
 #include "attn_tcgen05.cuh"

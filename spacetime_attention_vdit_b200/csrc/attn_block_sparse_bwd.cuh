@@ -26,8 +26,18 @@
 //
 // Measured: 32,760 tokens, 40 heads x 128, 32 of 256 blocks 8.7 to 9.1 ms (1.06 to
 // 1.11 PFLOP/s of the seven products), 43 % of it dq; a tile takes 1.3 us (dq) and 1.5
-// (dkv), a CTA's start and end 6 us.  Bound by the tensor pipe and its changes of
-// operand form: two a tile (dq), four (dkv).
+// (dkv), a CTA's start and end 6 us.  Bound at head_dim 128 by the tensor pipe and its
+// changes of operand form: two a tile (dq), four (dkv).  With half and a quarter of the
+// products a marked pair of blocks takes 2.6 us (head_dim 64) and 2.4 (32) in both
+// kernels together instead of 3.1 (148 x 4 blocks, 8 to 32 marked): there it is the chain
+// of a tile, S -> P -> dP -> dS -> product, one after another.
+//
+// A CTA per block, however many blocks its row or column marks: few query blocks (dq)
+// or few key blocks (dkv) leave SMs idle, and one column that every row marks is walked
+// by one CTA.  128 queries over 256 marked blocks, 12 heads x 128: 514 us; 128 keys
+// under 256 blocks of queries: 602; a window of 11 blocks at 32,760 tokens 966, with the
+// first key block marked by every row 1,405.  (The names carry the dense kernel's stem:
+// same CTA, same registers at launch.)
 #pragma once
 
 #include "attn_block_sparse.cuh"
@@ -408,8 +418,9 @@ __global__ void __launch_bounds__(384, 1)
 // dK, dV
 // ---------------------------------------------------------------------------
 //
-// Rows are keys.  TMEM is full (S^T, dP^T, dV and dK of 128 columns each at
-// head_dim 128), so nothing is double-buffered; the issue order
+// Rows are keys.  TMEM is full at head_dim 128 (S^T, dP^T, dV and dK of 128 columns
+// each), so nothing is double-buffered; smaller heads use the same places and leave
+// 128 (64) or 192 (32) columns idle.  The issue order
 //   dV_j, S_{j+1}, dK_j, dP_{j+1}
 // lets the elementwise warps exponentiate S_{j+1} under dK_j and dP_{j+1}, and
 // form dS_j under dV_j and S_{j+1}.

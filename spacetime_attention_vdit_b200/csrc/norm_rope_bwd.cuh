@@ -23,10 +23,11 @@
 //
 // Measured: 75,600 tokens x 5,120 channels, one group per token, Q and K: 912 to 972
 // us (4.8 to 5.1 TB/s, 0.73 to 0.78 of the copy rate); 7,800 x 12 x 128 per head: 41 us.
-// Bound by HBM in the end, but what had to be pared down is instructions: a
-// vector takes some 100 (half of them the formula's multiply-adds), and a warp
-// some 150 more per token for the sums, the barrier and the loop, which is why a
-// thread takes up to four vectors.
+// Bound by latency: a group has one token in flight, whose ten dependent shuffles,
+// barrier and shared-memory round trip leave about half of the issue slots empty.  What
+// had to be pared down before is instructions: a vector takes some 100 (half of them
+// the formula's multiply-adds), and a warp some 150 more per token for the sums, the
+// barrier and the loop, which is why a thread takes up to four vectors.
 #pragma once
 
 #include "patchify_rope.cuh"

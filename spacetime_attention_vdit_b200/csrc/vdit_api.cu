@@ -319,8 +319,10 @@ int rope_pass(const void* q_in, const void* k_in, void* q_out, void* k_out, int 
 // or alone if need be.  Measured (us, with and without): one token, 64 key blocks of
 // 32,760 keys, 12 heads in eights 18.6 / 110, 24 in fours 25.8 / 111, 48 in twos 43 /
 // 113, 100 alone 77 / 113; 1,560 queries, 20 key blocks, 4 heads in fours 30 / 45, but 8 heads in twos
-// 47.5 / 45.4: no twos for pairs of blocks.  16 heads in eights, which do not fit at
-// once, 35.5.
+// 47.5 / 45.4: no twos for pairs of blocks (that one size is all that was timed between
+// 36 and 148 pairs, where a CTA a pair takes 49 to 52).  16 heads in eights, which do
+// not fit at once, 35.5.  The rule knows the key blocks there are, not how many a row
+// marks: a token with two marked blocks takes a cluster of eight too.
 int sparse_splits(long long units, int nqb, int nkb, const int (&fit)[3]) {
   for (int i = 0, s = 8; s > 1; ++i, s /= 2)
     if (units <= fit[i] && nkb >= 2 * s && (s > 2 || nqb == 1)) return s;
